@@ -213,6 +213,113 @@ ws_status ws_decode_attention(const float *q, const float *k_new, const float *v
                               int s_max, void *workspace, size_t workspace_bytes,
                               ws_stream_t stream);
 
+/* Causal attention over packed prompts: token t of a sequence attends to that
+ * sequence's tokens up to and including t.  Query head h reads key-value head
+ * h / (n_heads / n_kv_heads) with scores q.k / sqrt(128) and an fp32 softmax.
+ * q [T][n_heads][128], k and v [T][n_kv_heads][128], bf16 or fp16 (dtype), a
+ * token's heads contiguous and tokens q_stride, k_stride, v_stride elements
+ * apart, so that the three may be columns of one fused projection's rows.
+ * cu_seqlens: int32 [n_seqs + 1] in device memory, read when the kernel runs:
+ * sequence i is the tokens cu_seqlens[i] .. cu_seqlens[i + 1] - 1 (none where
+ * the two are equal).  A sequence whose bounds are out of order or outside
+ * 0 .. T is skipped and raises the device error flag (3).  out [T][n_heads *
+ * 128] of the same type; lse fp32 [T][n_heads], the natural logarithm of each
+ * row's sum of e^score, or NULL.  Rows of out and lse outside every sequence
+ * are left as they were, and what q, k and v hold there is not used; a value
+ * that is not finite reaches only the tokens that attend to it.
+ * head_dim must be 128, n_heads a multiple of n_kv_heads; the four matrices
+ * 16-byte aligned, strides a multiple of 8 and at least the heads'
+ * dimensions.  The probabilities enter the second product in q's type,
+ * everything else is held in fp32. */
+ws_status ws_prompt_attention(const void *q, const void *k, const void *v, int dtype,
+                              const int32_t *cu_seqlens, void *out, float *lse, int T, int n_seqs,
+                              int n_heads, int n_kv_heads, int head_dim, long long q_stride,
+                              long long k_stride, long long v_stride, ws_stream_t stream);
+
+/* A key-value cache held in 4 bits: k_cache and v_cache uint8
+ * [rows][n_kv_heads][s_max][80], 16-byte aligned.  A row of 80 bytes is one
+ * slot's 128 values in four groups of 32 consecutive dimensions: 64 bytes of
+ * codes, then the groups' bf16 (s, z) pairs (s first); code q (0..15) stands
+ * for s * (q - 8) + z, computed in fp32.  Codes of a key row: 32-bit
+ * little-endian word 4t + g holds dimensions 32g + 8t .. + 7 (t, g in 0..3),
+ * bits 4i .. 4i+3 dimension i of those; of a value row: 16-bit unit 4r + g
+ * holds dimensions 32g + 4r .. + 3 (r in 0..7), bits 4i .. 4i+3 dimension i.
+ * Rows are quantised min-max per group with every decision in fp32:
+ * s = bf16((max - min) / 15), 0 where that is below 2^-126;
+ * z = bf16(min + 8 s); q = clamp(rint((x - z) / s) + 8, 0, 15), 8 where s is
+ * 0.  A group with a value that is not finite stands for NaN as a whole.
+ *
+ * ws_kv_store_q4: k and v [T][n_kv_heads][128] (fp32, bf16 or fp16; a token's
+ * heads contiguous, tokens k_stride and v_stride elements apart) into the
+ * cache.  cu_seqlens (int32 [n_seqs + 1] on the device): token t of sequence
+ * i goes to slot start[i] + t - cu_seqlens[i] of cache row rows[i]; NULL:
+ * T = n_seqs and token i is sequence i, one new token for each.  rows (int32
+ * [n_seqs] on the device): NULL takes row i for sequence i.  start (int32
+ * [n_seqs] on the device): negative skips the sequence.  Tokens outside every
+ * sequence are skipped; one whose row is outside 0 .. n_rows - 1 or whose
+ * slot is outside 0 .. s_max - 1 is skipped and raises the device error flag
+ * (2).  Two tokens of one call must not share a slot.
+ * ws_kv_load_q4: the reverse, with the same arguments: the values that the
+ * rows stand for, rounded once to dtype, to k and v contiguous [T][n_kv_heads]
+ * [128]; skipped tokens are left as they were.
+ * head_dim must be 128, n_kv_heads at most 65535, strides a multiple of 8,
+ * every matrix 16-byte aligned.  ws_kv_q4_row_bytes: 80, or 0 for another
+ * head_dim. */
+size_t ws_kv_q4_row_bytes(int head_dim);
+ws_status ws_kv_store_q4(const void *k, const void *v, int dtype, const int32_t *cu_seqlens,
+                         const int32_t *rows, const int32_t *start, void *k_cache, void *v_cache,
+                         int T, int n_seqs, int n_rows, int n_kv_heads, int head_dim, int s_max,
+                         long long k_stride, long long v_stride, ws_stream_t stream);
+ws_status ws_kv_load_q4(const void *k_cache, const void *v_cache, const int32_t *cu_seqlens,
+                        const int32_t *rows, const int32_t *start, void *k, void *v, int dtype,
+                        int T, int n_seqs, int n_rows, int n_kv_heads, int head_dim, int s_max,
+                        ws_stream_t stream);
+
+/* ws_decode_attention over the 4-bit cache: per batch row b the new key and
+ * value (fp32 [B][n_kv_heads * 128]) are quantised into slot pos[b] (the same
+ * bytes as ws_kv_store_q4 writes), and query head h attends over slots
+ * 0 .. pos[b] of the values that the rows stand for.  pos: int32 [B] on the
+ * device, read when the kernel runs; a negative position marks a batch row
+ * without a sequence, which is left as it is; one past s_max - 1 skips the
+ * row and raises the device error flag (2).  Slots after pos are never read.
+ * q and the probabilities enter the products as bf16 hi + lo pairs (relative
+ * error 2^-17), the codes exactly; scores, softmax and sums are fp32.
+ * out_f32 and/or out_bf16 [B][n_heads * 128]; either may be NULL, not both.
+ * 1 <= B <= 1024, head_dim 128, n_heads / n_kv_heads at most 8, any s_max;
+ * every matrix 16-byte aligned.  Workspace (zero-filled before its first use,
+ * left ready for the next call by every call): ws_attention_q4_workspace_bytes(B,
+ * n_heads, n_kv_heads, 128, s_max); calls that share one must not overlap. */
+size_t ws_attention_q4_workspace_bytes(int B, int n_heads, int n_kv_heads, int head_dim,
+                                       int s_max);
+ws_status ws_decode_attention_q4(const float *q, const float *k_new, const float *v_new,
+                                 void *k_cache, void *v_cache, const int32_t *pos, float *out_f32,
+                                 void *out_bf16, int B, int n_heads, int n_kv_heads, int head_dim,
+                                 int s_max, void *workspace, size_t workspace_bytes,
+                                 ws_stream_t stream);
+
+/* Log-probabilities over rows of logits (fp32, bf16 or fp16; V values a row,
+ * rows ld >= V elements apart; the ones behind V are not read).  With
+ * p = softmax of the row, everything natural and in fp32:
+ *  - logprob[r] = log p[targets[r]] (both int32 / fp32 [rows], or both NULL);
+ *    0 where the target is negative (no token), NaN and the device error flag
+ *    (4) where it is V or more;
+ *  - entropy[r] = -sum p log p, terms of p = 0 being 0 (fp32 [rows] or NULL);
+ *  - top_idx, top_logprob [rows][topk] (int32, fp32; topk 0..32 and at most V;
+ *    either may be NULL): the topk largest logits in falling order, equal ones
+ *    by the lower index, and their log-probabilities.
+ * A logit of -infinity is a token ruled out (p = 0).  A row that holds a NaN
+ * or +infinity, or nothing but -infinity, has NaN log-probabilities and
+ * entropy; its alternatives are still ordered, a NaN never among them (places
+ * left over: index -1, NaN).
+ * Workspace (zero-filled before its first use, left ready for the next call
+ * by every call): ws_logprobs_workspace_bytes(rows, V, topk), 0 for sizes
+ * that the call refuses; calls that share one must not overlap. */
+size_t ws_logprobs_workspace_bytes(int rows, int V, int topk);
+ws_status ws_token_logprobs(const void *logits, int dtype, long long ld, const int32_t *targets,
+                            float *logprob, float *entropy, int32_t *top_idx, float *top_logprob,
+                            int rows, int V, int topk, void *workspace, size_t workspace_bytes,
+                            ws_stream_t stream);
+
 /* idx[r] = the lowest j with v[r][j] == max_j v[r][j] for fp32 rows
  * [rows][cols] ("One Token, Kernel by Kernel", "The whole step").  Workspace
  * required: ws_workspace_bytes(WS_OP_ARGMAX_ROWS, rows, cols, 1). */
@@ -509,8 +616,9 @@ size_t ws_workspace_bytes(int op, int M, int K, int B);
 
 const char *ws_last_error(void);
 
-/* Device error flag of the current device (nonzero after a bounded wait ran
- * out); reset != 0 clears it.  Synchronises the device.  Returns -1 if the
+/* Device error flag of the current device: 1 after a bounded wait ran out, 2
+ * after a position or slot outside its cache, 3 after sequence bounds out of
+ * order or range, 4 after a token outside the vocabulary; reset != 0 clears it.  Synchronises the device.  Returns -1 if the
  * flag cannot be read. */
 int ws_device_error(int reset);
 

@@ -23,6 +23,7 @@ P = C.c_void_p
 I32 = C.c_int
 SZ = C.c_size_t
 F32 = C.c_float
+LL = C.c_longlong
 
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 PREFETCH_NONE, PREFETCH_L2, PREFETCH_L2_EVICT_LAST, PREFETCH_BULK = 0, 1, 2, 3
@@ -112,6 +113,11 @@ _SIGS = {
     "ws_lmhead_argmax": [P, I32, P, P, P, P, I32, I32, I32, F32, P, SZ, P],
     "ws_argmax_rows": [P, P, I32, I32, P, SZ, P],
     "ws_decode_attention": [P, P, P, P, P, P, P, P, I32, I32, I32, I32, I32, P, SZ, P],
+    "ws_prompt_attention": [P, P, P, I32, P, P, P, I32, I32, I32, I32, I32, LL, LL, LL, P],
+    "ws_kv_store_q4": [P, P, I32, P, P, P, P, P, I32, I32, I32, I32, I32, I32, LL, LL, P],
+    "ws_kv_load_q4": [P, P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I32, P],
+    "ws_decode_attention_q4": [P, P, P, P, P, P, P, P, I32, I32, I32, I32, I32, P, SZ, P],
+    "ws_token_logprobs": [P, I32, LL, P, P, P, P, P, I32, I32, I32, P, SZ, P],
     "ws_quantize_q4": [P, P, I32, I32, P],
     "ws_gemv_q4": [P, P, P, I32, I32, I32, P, SZ, P],
     "ws_rmsnorm": [P, P, P, I32, I32, I32, F32, P],
@@ -138,6 +144,9 @@ _SIGS = {
 _OTHER = {
     "ws_workspace_bytes": ([I32, I32, I32, I32], SZ),
     "ws_attention_workspace_bytes": ([I32, I32, I32, I32, I32], SZ),
+    "ws_attention_q4_workspace_bytes": ([I32, I32, I32, I32, I32], SZ),
+    "ws_logprobs_workspace_bytes": ([I32, I32, I32], SZ),
+    "ws_kv_q4_row_bytes": ([I32], SZ),
     "ws_q4_row_bytes": ([I32], SZ),
     "ws_last_error": ([], C.c_char_p),
     "ws_device_error": ([I32], I32),
@@ -334,6 +343,161 @@ def decode_attention(q, k_new, v_new, k_cache, v_cache, pos, workspace, out_f32=
     _check(load().ws_decode_attention(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache),
                                       _ptr(v_cache), _ptr(pos), _ptr(out_f32), _ptr(out_bf16),
                                       B, n_heads, n_kv, d, s_max, wp, wb, _stream(stream)))
+
+
+def _here(*tensors):
+    """Refuse tensors that are not on the current device (the library launches there)."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensor on {t.device}: expected the current device, cuda:{dev}")
+
+
+def _need(ok, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _whole(t, dtype, shape, what: str):
+    """Refuse a tensor that is not contiguous, of this type and shape; None passes."""
+    if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
+        raise ValueError(f"{what}: expected contiguous {dtype} {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+
+
+def _token_heads(t, what: str):
+    """[T, heads, d] with each token's heads contiguous -> (T, heads, d, token stride)."""
+    if t.dim() != 3:
+        raise ValueError(f"{what}: expected [tokens, heads, head_dim], got {tuple(t.shape)}")
+    T, n, d = t.shape
+    st, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and n > 1):
+        raise ValueError(f"{what}: a token's heads must be contiguous, got strides {t.stride()}")
+    return T, n, d, (st if T > 1 else n * d)
+
+
+def prompt_attention(q, k, v, cu_seqlens, out, lse=None, stream=None):
+    """Causal attention over packed prompts.  q [T, n_heads, 128], k and v
+    [T, n_kv, 128] in bf16 or fp16 (token strides free, so columns of one
+    fused projection will do), cu_seqlens int32 [n_seqs + 1] on the device,
+    out [T, n_heads * 128] of the same type, lse fp32 [T, n_heads] or None."""
+    T, nh, d, qs = _token_heads(q, "q")
+    Tk, nkv, dk, ks = _token_heads(k, "k")
+    Tv, nv, dv, vs = _token_heads(v, "v")
+    _need(Tk == T == Tv and nv == nkv and dk == d == dv, "q, k and v disagree in shape")
+    _need(k.dtype == q.dtype == v.dtype, "q, k and v disagree in type")
+    _whole(out, q.dtype, (T, nh * d), "out")
+    _whole(lse, torch.float32, (T, nh), "lse")
+    _need(cu_seqlens.dim() == 1, "cu_seqlens: expected one dimension")
+    _whole(cu_seqlens, torch.int32, cu_seqlens.shape, "cu_seqlens")
+    _here(q, k, v, cu_seqlens, out, lse)
+    _check(load().ws_prompt_attention(_ptr(q), _ptr(k), _ptr(v), _dtype_code(q), _ptr(cu_seqlens),
+                                      _ptr(out), _ptr(lse), T, cu_seqlens.shape[0] - 1, nh, nkv,
+                                      d, qs, ks, vs, _stream(stream)))
+
+
+def kv_q4_row_bytes(head_dim=128) -> int:
+    return int(load().ws_kv_q4_row_bytes(head_dim))
+
+
+def new_kv_cache_q4(n_rows, n_kv_heads, s_max, head_dim=128, device="cuda"):
+    """One 4-bit cache (keys or values): uint8 [n_rows, n_kv, s_max, 80]."""
+    return torch.zeros((n_rows, n_kv_heads, s_max, kv_q4_row_bytes(head_dim)), dtype=torch.uint8,
+                       device=device)
+
+
+def _kv_q4_args(T, nkv, k_cache, v_cache, start, cu_seqlens, rows):
+    n_rows, n, s_max, rb = k_cache.shape
+    _need(rb == kv_q4_row_bytes() and n == nkv, "k_cache: expected [rows, n_kv, s_max, 80]")
+    _whole(k_cache, torch.uint8, k_cache.shape, "k_cache")
+    _whole(v_cache, torch.uint8, k_cache.shape, "v_cache")
+    n_seqs = start.shape[0]
+    _whole(start, torch.int32, (n_seqs,), "start")
+    _whole(rows, torch.int32, (n_seqs,), "rows")
+    _whole(cu_seqlens, torch.int32, (n_seqs + 1,), "cu_seqlens")
+    return n_seqs, n_rows, s_max
+
+
+def kv_store_q4(k, v, k_cache, v_cache, start, cu_seqlens=None, rows=None, stream=None):
+    """k, v [T, n_kv, 128] (fp32, bf16 or fp16) into the 4-bit caches uint8
+    [n_rows, n_kv, s_max, 80] from slot start[i] on of cache row rows[i] (i
+    without `rows`) for the tokens cu_seqlens[i] .. cu_seqlens[i + 1] - 1
+    (token i alone without `cu_seqlens`)."""
+    T, nkv, d, ks = _token_heads(k, "k")
+    Tv, nv, dv, vs = _token_heads(v, "v")
+    _need(Tv == T and nv == nkv and dv == d and v.dtype == k.dtype, "k and v disagree")
+    n_seqs, n_rows, s_max = _kv_q4_args(T, nkv, k_cache, v_cache, start, cu_seqlens, rows)
+    _here(k, v, k_cache, v_cache, start, cu_seqlens, rows)
+    _check(load().ws_kv_store_q4(_ptr(k), _ptr(v), _dtype_code(k), _ptr(cu_seqlens), _ptr(rows),
+                                 _ptr(start), _ptr(k_cache), _ptr(v_cache), T, n_seqs, n_rows,
+                                 nkv, d, s_max, ks, vs, _stream(stream)))
+
+
+def kv_load_q4(k_cache, v_cache, start, k, v, cu_seqlens=None, rows=None, stream=None):
+    """The values that cached rows stand for, to k and v [T, n_kv, 128] (fp32,
+    bf16 or fp16, contiguous); the other arguments as for kv_store_q4."""
+    T, nkv, d, _ = _token_heads(k, "k")
+    _whole(k, k.dtype, k.shape, "k")
+    _whole(v, k.dtype, k.shape, "v")
+    n_seqs, n_rows, s_max = _kv_q4_args(T, nkv, k_cache, v_cache, start, cu_seqlens, rows)
+    _here(k, v, k_cache, v_cache, start, cu_seqlens, rows)
+    _check(load().ws_kv_load_q4(_ptr(k_cache), _ptr(v_cache), _ptr(cu_seqlens), _ptr(rows),
+                                _ptr(start), _ptr(k), _ptr(v), _dtype_code(k), T, n_seqs, n_rows,
+                                nkv, d, s_max, _stream(stream)))
+
+
+def attention_q4_workspace_bytes(B, n_heads, n_kv_heads, s_max, head_dim=128) -> int:
+    return int(load().ws_attention_q4_workspace_bytes(B, n_heads, n_kv_heads, head_dim, s_max))
+
+
+def decode_attention_q4(q, k_new, v_new, k_cache, v_cache, pos, workspace, out_f32=None,
+                        out_bf16=None, stream=None):
+    """decode_attention over the 4-bit caches uint8 [B, n_kv, s_max, 80]: q
+    [B, n_heads*128] fp32, k_new/v_new [B, n_kv*128] fp32 (quantised into the
+    caches at pos), pos int32 [B] on the device (negative: no sequence)."""
+    B, nkv, s_max, rb = k_cache.shape
+    d = 128
+    nh = q.shape[1] // d
+    _need(rb == kv_q4_row_bytes(), "k_cache: expected [B, n_kv, s_max, 80]")
+    _whole(k_cache, torch.uint8, k_cache.shape, "k_cache")
+    _whole(v_cache, torch.uint8, k_cache.shape, "v_cache")
+    _whole(q, torch.float32, (B, nh * d), "q")
+    _whole(k_new, torch.float32, (B, nkv * d), "k_new")
+    _whole(v_new, torch.float32, (B, nkv * d), "v_new")
+    _whole(pos, torch.int32, (B,), "pos")
+    _whole(out_f32, torch.float32, (B, nh * d), "out_f32")
+    _whole(out_bf16, torch.bfloat16, (B, nh * d), "out_bf16")
+    _here(q, k_new, v_new, k_cache, v_cache, pos, workspace, out_f32, out_bf16)
+    wp, wb = _ws(workspace)
+    _check(load().ws_decode_attention_q4(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache),
+                                         _ptr(v_cache), _ptr(pos), _ptr(out_f32), _ptr(out_bf16),
+                                         B, nh, nkv, d, s_max, wp, wb, _stream(stream)))
+
+
+def logprobs_workspace_bytes(rows, V, topk=0) -> int:
+    return int(load().ws_logprobs_workspace_bytes(rows, V, topk))
+
+
+def token_logprobs(logits, workspace, targets=None, logprob=None, entropy=None, top_idx=None,
+                   top_logprob=None, stream=None):
+    """Log-probabilities over logits [rows, V] (fp32, bf16 or fp16; rows may be
+    padded): logprob fp32 [rows] of targets int32 [rows], entropy fp32 [rows],
+    top_idx int32 and top_logprob fp32 [rows, topk]; each output may be None."""
+    rows, V = logits.shape
+    _need(logits.stride(1) == 1 or V == 1, "logits: a row's values must be contiguous")
+    ld = logits.stride(0) if rows > 1 else V
+    top = top_idx if top_idx is not None else top_logprob
+    topk = 0 if top is None else top.shape[1]
+    _whole(targets, torch.int32, (rows,), "targets")
+    _whole(logprob, torch.float32, (rows,), "logprob")
+    _whole(entropy, torch.float32, (rows,), "entropy")
+    _whole(top_idx, torch.int32, (rows, topk), "top_idx")
+    _whole(top_logprob, torch.float32, (rows, topk), "top_logprob")
+    _here(logits, workspace, targets, logprob, entropy, top_idx, top_logprob)
+    wp, wb = _ws(workspace)
+    _check(load().ws_token_logprobs(_ptr(logits), _dtype_code(logits), ld, _ptr(targets),
+                                    _ptr(logprob), _ptr(entropy), _ptr(top_idx),
+                                    _ptr(top_logprob), rows, V, topk, wp, wb, _stream(stream)))
 
 
 def rmsnorm(x, gamma, y, eps, stream=None):

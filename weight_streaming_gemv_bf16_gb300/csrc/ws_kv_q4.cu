@@ -1,0 +1,200 @@
+// ws_kv_q4.cu -- rows into the 4-bit key-value cache and out of it: packed
+// prompts, or one token per cache row, as keys and values in fp32, bf16 or
+// fp16; and the cached rows back as the values they stand for.
+//
+// Bound by DRAM: a token and key-value head reads 512 bytes (16-bit) and
+// writes 160.  A warp takes one token and head, lanes 0..15 its key row and
+// 16..31 its value row, eight dimensions a lane, so that a group of 32 is a
+// quad: its minimum and maximum are two shuffles away and nothing passes
+// through shared memory.  A CTA's warps take consecutive tokens of one head:
+// their rows are neighbours in the cache.
+#include "ws_kv_q4.cuh"
+
+#include "wsgemv.h"
+
+namespace ws {
+
+struct KvRowsParams {
+  const void* k;  // [T] tokens of [nkv][128], strides in elements
+  const void* v;
+  void* k_out;  // load: contiguous [T][nkv][128]
+  void* v_out;
+  const int* cu;     // [n + 1] token bounds of the sequences; null: token i is sequence i
+  const int* rows;   // [n] cache row of each sequence; null: row i
+  const int* start;  // [n] slot of its first token, negative: none
+  unsigned char* kc;  // [n_rows][nkv][S][80]
+  unsigned char* vc;
+  long long ks, vs;
+  int T, n, n_rows, nkv, S;
+  int* err;
+};
+
+// Cache row and slot of token t; false where it has none.  bad: a row or slot
+// outside the cache (no access is made there).
+__device__ __forceinline__ bool kv_place(const KvRowsParams& a, int t, int& row, int& slot,
+                                         bool& bad) {
+  int i = t, off = 0;
+  bad = false;
+  if (a.cu) {
+    int lo = 0, hi = a.n;  // the last bound at or before t
+    if (a.cu[0] > t) return false;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.cu[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    if (lo >= a.n || a.cu[lo + 1] <= t) return false;
+    i = lo;
+    off = t - a.cu[lo];
+  }
+  const int s0 = a.start[i];
+  if (s0 < 0) return false;
+  row = a.rows ? a.rows[i] : i;
+  bad = row < 0 || row >= a.n_rows || s0 >= a.S || off >= a.S - s0;
+  slot = s0 + off;
+  return !bad;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(256) k_kv_store_q4(const __grid_constant__ KvRowsParams a) {
+  const int t = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, g = blockIdx.y;
+  if (t >= a.T) return;
+  int row, slot;
+  bool bad;
+  if (!kv_place(a, t, row, slot, bad)) {
+    if (bad && lane == 0) atomicExch(a.err, kDerrBadSlot);
+    return;
+  }
+  const bool keys = lane < 16;
+  const size_t es = DT == DT_F32 ? 4 : 2;
+  const char* src = static_cast<const char*>(keys ? a.k : a.v) +
+                    ((size_t)t * (keys ? a.ks : a.vs) + (size_t)g * kKvDim + (lane & 15) * 8) * es;
+  float x[8];
+  load8<DT>(src, x);
+  uint32_t sz;
+  const uint32_t w = quantize8(x, sz);
+  unsigned char* dst = (keys ? a.kc : a.vc) + (((size_t)row * a.nkv + g) * a.S + slot) * kKvRow;
+  put_row(dst, w, sz, keys, true);
+}
+
+template <int DT>
+__global__ void __launch_bounds__(256) k_kv_load_q4(const __grid_constant__ KvRowsParams a) {
+  const int t = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, g = blockIdx.y;
+  if (t >= a.T) return;
+  int row, slot;
+  bool bad;
+  if (!kv_place(a, t, row, slot, bad)) {
+    if (bad && lane == 0) atomicExch(a.err, kDerrBadSlot);
+    return;
+  }
+  const bool keys = lane < 16;
+  const size_t es = DT == DT_F32 ? 4 : 2;
+  const unsigned char* src =
+      (keys ? a.kc : a.vc) + (((size_t)row * a.nkv + g) * a.S + slot) * kKvRow;
+  float x[8];
+  get_row(src, keys, x);
+  char* dst = static_cast<char*>(keys ? a.k_out : a.v_out) +
+              (((size_t)t * a.nkv + g) * kKvDim + (lane & 15) * 8) * es;
+  store8<DT>(dst, x);
+}
+
+static bool misaligned(const void* p) { return ((uintptr_t)p & 15u) != 0; }
+
+static ws_status kv_rows(KvRowsParams& a, int dtype, int head_dim, bool store,
+                         cudaStream_t stream) {
+  const void* k = store ? a.k : a.k_out;
+  const void* v = store ? a.v : a.v_out;
+  if (!k || !v || !a.kc || !a.vc || !a.start) {
+    set_error("null argument");
+    return WS_ERR_ARG;
+  }
+  if (dtype != WS_DTYPE_F32 && dtype != WS_DTYPE_BF16 && dtype != WS_DTYPE_F16) {
+    set_error("dtype must be WS_DTYPE_F32, WS_DTYPE_BF16 or WS_DTYPE_F16");
+    return WS_ERR_ARG;
+  }
+  if (a.T < 1 || a.n < 1 || a.n_rows < 1 || a.nkv < 1 || a.nkv > 65535 || a.S < 1 ||
+      head_dim != kKvDim || (!a.cu && a.T != a.n) ||
+      (store && (a.ks < (long long)a.nkv * kKvDim || a.vs < (long long)a.nkv * kKvDim ||
+                 a.ks % 8 || a.vs % 8))) {
+    set_error("4-bit rows: T, sequences, rows, key-value heads (to 65535) and s_max at least 1, "
+              "head_dim %d, T = sequences without bounds, token strides a multiple of 8 and at "
+              "least n_kv_heads * %d", kKvDim, kKvDim);
+    return WS_ERR_SHAPE;
+  }
+  if (misaligned(k) || misaligned(v) || misaligned(a.kc) || misaligned(a.vc)) {
+    set_error("4-bit rows: keys, values and caches must be 16-byte aligned");
+    return WS_ERR_ALIGN;
+  }
+  a.err = device_error_ptr();
+  if (!a.err) {
+    set_error("device error flag unavailable");
+    return WS_ERR_CUDA;
+  }
+  const dim3 grid((a.T + 7) / 8, a.nkv);
+  if (store) {
+    if (dtype == WS_DTYPE_F32) k_kv_store_q4<DT_F32><<<grid, 256, 0, stream>>>(a);
+    else if (dtype == WS_DTYPE_BF16) k_kv_store_q4<DT_BF16><<<grid, 256, 0, stream>>>(a);
+    else k_kv_store_q4<DT_F16><<<grid, 256, 0, stream>>>(a);
+  } else {
+    if (dtype == WS_DTYPE_F32) k_kv_load_q4<DT_F32><<<grid, 256, 0, stream>>>(a);
+    else if (dtype == WS_DTYPE_BF16) k_kv_load_q4<DT_BF16><<<grid, 256, 0, stream>>>(a);
+    else k_kv_load_q4<DT_F16><<<grid, 256, 0, stream>>>(a);
+  }
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    set_error("launch failed: %s", cudaGetErrorString(e));
+    return WS_ERR_CUDA;
+  }
+  return WS_OK;
+}
+
+}  // namespace ws
+
+using namespace ws;
+
+extern "C" {
+
+size_t ws_kv_q4_row_bytes(int head_dim) { return head_dim == kKvDim ? kKvRow : 0; }
+
+ws_status ws_kv_store_q4(const void *k, const void *v, int dtype, const int32_t *cu_seqlens,
+                         const int32_t *rows, const int32_t *start, void *k_cache, void *v_cache,
+                         int T, int n_seqs, int n_rows, int n_kv_heads, int head_dim, int s_max,
+                         long long k_stride, long long v_stride, ws_stream_t stream) {
+  KvRowsParams a = {};
+  a.k = k;
+  a.v = v;
+  a.cu = cu_seqlens;
+  a.rows = rows;
+  a.start = start;
+  a.kc = static_cast<unsigned char*>(k_cache);
+  a.vc = static_cast<unsigned char*>(v_cache);
+  a.ks = k_stride;
+  a.vs = v_stride;
+  a.T = T;
+  a.n = n_seqs;
+  a.n_rows = n_rows;
+  a.nkv = n_kv_heads;
+  a.S = s_max;
+  return kv_rows(a, dtype, head_dim, true, (cudaStream_t)stream);
+}
+
+ws_status ws_kv_load_q4(const void *k_cache, const void *v_cache, const int32_t *cu_seqlens,
+                        const int32_t *rows, const int32_t *start, void *k, void *v, int dtype,
+                        int T, int n_seqs, int n_rows, int n_kv_heads, int head_dim, int s_max,
+                        ws_stream_t stream) {
+  KvRowsParams a = {};
+  a.k_out = k;
+  a.v_out = v;
+  a.cu = cu_seqlens;
+  a.rows = rows;
+  a.start = start;
+  a.kc = static_cast<unsigned char*>(const_cast<void*>(k_cache));
+  a.vc = static_cast<unsigned char*>(const_cast<void*>(v_cache));
+  a.T = T;
+  a.n = n_seqs;
+  a.n_rows = n_rows;
+  a.nkv = n_kv_heads;
+  a.S = s_max;
+  return kv_rows(a, dtype, head_dim, false, (cudaStream_t)stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,175 @@
+// ws_kv_q4.cuh -- the 4-bit key-value row: its layout and its quantiser,
+// shared by the row store and load (ws_kv_q4.cu) and the decode attention
+// over such a cache (ws_attention_q4.cu).
+//
+// A row is one slot of one key-value head: 128 values in four groups of 32
+// consecutive dimensions, each with a bf16 scale s and zero z; code q (0..15)
+// stands for s (q - 8) + z, the reading of the library's 4-bit weights at a
+// finer group (a key's channels differ more than a weight's columns, and 32
+// values is as many as one quad of lanes quantises without leaving its
+// registers).  64 bytes of codes, then four (s, z) pairs: 80 bytes, an odd
+// multiple of 16, so that the 16-byte pieces of 8 rows lie in distinct
+// shared-memory banks.  The order of the codes is that of the decode
+// attention's matrix products, so that their operands come from few wide
+// loads with no exchange between lanes:
+//   keys:   32-bit word 4 t + g holds dimensions 32 g + 8 t .. + 7 (t, g in
+//           0..3; lane t of a quad reads its words of all four groups as 16
+//           bytes), bits 4 i .. 4 i + 3 dimension i of the eight;
+//   values: 16-bit unit 4 r + g holds dimensions 32 g + 4 r .. + 3 (r in
+//           0..7; lane r reads its units of all four groups as 8 bytes), bits
+//           4 i .. 4 i + 3 dimension i of the four.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cfloat>
+
+#include "ws_common.cuh"
+#include "ws_device.cuh"
+
+namespace ws {
+
+constexpr int kKvDim = 128;
+constexpr int kKvGroup = 32;
+constexpr int kKvCodes = kKvDim / 2;                              // bytes of codes
+constexpr int kKvRow = kKvCodes + kKvDim / kKvGroup * 4;          // 80
+constexpr int kDerrBadSlot = 2;                                   // a position or slot outside the cache
+constexpr int kDerrBadSeq = 3;                                    // sequence bounds out of order or range
+constexpr int kDerrBadToken = 4;                                  // a token outside the vocabulary
+constexpr uint32_t kBf16Nan = 0x7fc0u;
+
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Eight consecutive values (dimensions 8 l .. 8 l + 7 of a row, l = lane % 16,
+// 16 lanes a row; both halves of the warp take part) to their codes, nibble i
+// dimension i, and the group's (s, z) as bits s | z << 16.  Every decision in
+// fp32: s = bf16((max - min) / 15), taken as 0 below 2^-126; z = bf16(min +
+// 8 s); q = clamp(rint((x - z) / s) + 8, 0, 15), 8 where s is 0.  A group
+// with a value that is not finite stands for NaN as a whole.
+__device__ __forceinline__ uint32_t quantize8(const float (&x)[8], uint32_t& sz) {
+  float lo = x[0], hi = x[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    lo = min_nan(lo, x[i]);
+    hi = max_nan(hi, x[i]);
+  }
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  const float s32 = __fdiv_rn(__fsub_rn(hi, lo), 15.f);
+  if (!(s32 <= FLT_MAX)) {  // a NaN or an infinity in the group
+    sz = kBf16Nan | (kBf16Nan << 16);
+    return 0x88888888u;
+  }
+  float s = __bfloat162float(__float2bfloat16_rn(s32));
+  if (s < 1.17549435e-38f) s = 0.f;
+  const float z = __bfloat162float(__float2bfloat16_rn(__fadd_rn(lo, 8.f * s)));
+  sz = (__float_as_uint(s) >> 16) | (__float_as_uint(z) & 0xffff0000u);
+  if (s == 0.f) return 0x88888888u;
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float q = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[i], z), s)) + 8.f, 0.f), 15.f);
+    w |= (uint32_t)q << (4 * i);
+  }
+  return w;
+}
+
+// The row's 80 bytes from 16 lanes' quantize8 results: lane l = 4 g + t of the
+// half warp holds the codes of group g.  `row` in global or shared memory,
+// 4-byte aligned; write = false takes part in the exchange only.
+__device__ __forceinline__ void put_row(unsigned char* row, uint32_t w, uint32_t sz, bool keys,
+                                        bool write) {
+  const int l = threadIdx.x & 15, g = l >> 2, t = l & 3;
+  // values: the pair of groups (g, g ^ 1) trades halves, so that each lane
+  // writes the two units of one r
+  const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 4);
+  int at = 4 * t + g;
+  if (!keys) {
+    if (g & 1) {
+      w = (other >> 16) | (w & 0xffff0000u);
+      at = (2 * t + 1) * 2 + (g >> 1);
+    } else {
+      w = (w & 0xffffu) | (other << 16);
+      at = (2 * t) * 2 + (g >> 1);
+    }
+  }
+  if (!write) return;
+  reinterpret_cast<uint32_t*>(row)[at] = w;
+  if (t == 0) reinterpret_cast<uint32_t*>(row + kKvCodes)[g] = sz;
+}
+
+// The eight values that lane l of a row's 16 lanes stores and reads.
+__device__ __forceinline__ void get_row(const unsigned char* row, bool keys, float (&x)[8]) {
+  const int l = threadIdx.x & 15, g = l >> 2, t = l & 3;
+  uint32_t w;
+  if (keys) {
+    w = reinterpret_cast<const uint32_t*>(row)[4 * t + g];
+  } else {
+    const uint16_t* u = reinterpret_cast<const uint16_t*>(row);
+    w = u[4 * (2 * t) + g] | ((uint32_t)u[4 * (2 * t + 1) + g] << 16);
+  }
+  const uint32_t sz = reinterpret_cast<const uint32_t*>(row + kKvCodes)[g];
+  const float s = bf16lo(sz), z = bf16hi(sz);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    x[i] = __fadd_rn(__fmul_rn(s, (float)((int)((w >> (4 * i)) & 15u) - 8)), z);
+}
+
+template <int DT>
+__device__ __forceinline__ void load8(const void* p, float (&x)[8]) {
+  if constexpr (DT == DT_F32) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (DT == DT_F16) {
+        const __half2 h = *reinterpret_cast<const __half2*>(&w[j]);
+        x[2 * j] = __low2float(h);
+        x[2 * j + 1] = __high2float(h);
+      } else {
+        x[2 * j] = bf16lo(w[j]);
+        x[2 * j + 1] = bf16hi(w[j]);
+      }
+    }
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(void* p, const float (&x)[8]) {
+  if constexpr (DT == DT_F32) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (DT == DT_F16) {
+        const __half2 h = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+}  // namespace ws
