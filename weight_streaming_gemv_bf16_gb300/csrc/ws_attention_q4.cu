@@ -4,6 +4,7 @@
 // out_h = sum_j p_j v_j, p = softmax_j(q_h . k_j / sqrt(128)) over the slots
 // 0 .. pos, k and v = s (code - 8) + z per slot and group of 32 dimensions.
 #include <cmath>
+#include <mutex>
 
 #include "ws_kv_q4.cuh"
 
@@ -11,9 +12,21 @@
 
 namespace ws {
 
-constexpr int kQ4MaxG = 8;       // query heads per key-value head
+constexpr int kQ4MaxG = 8;       // query heads per key-value head (half the MMA's 16 rows)
 constexpr int kQ4MaxB = 1024;
-constexpr int kQ4Tile = 128;
+constexpr int kQ4Tile = 16;      // slots per tile
+constexpr int kQ4Warps = 4;
+constexpr int kQ4Threads = kQ4Warps * 32;
+constexpr int kQ4Stages = 4;     // ring stages per warp
+constexpr int kQ4StageBytes = 2 * kQ4Tile * kKvRow;  // keys, then values
+constexpr int kQ4MaxCtas = 1024;
+constexpr int kQ4MinTiles = 2 * kQ4Warps;            // tiles a CTA takes at least
+constexpr int kQ4Merge = 16;                         // partial results merged in one go
+constexpr int kQ4Part = kKvDim + 2;                  // one partial result: acc[128], max, sum
+constexpr int kQ4Ring = kQ4Warps * kQ4Stages * kQ4StageBytes;
+constexpr int kQ4Smem = kQ4Ring + kQ4Warps * kQ4MaxG * kKvDim * 4;
+// the running maximum follows the tile's only when that is 2^8 above it
+constexpr float kQ4Lazy = 8.f;
 
 struct AttnQ4Params {
   const float* q;      // [B][nh * 128]
@@ -24,96 +37,492 @@ struct AttnQ4Params {
   const int* pos;      // [B]: slot of the new token, negative: none
   float* out_f32;
   uint16_t* out_bf16;
-  int nh, nkv, S, G;
-  float scale;
+  int B, nh, nkv, S, G;
+  float scale;         // log2(e) / sqrt(128)
+  float* part;         // [CTAs][2][G][130]
+  unsigned* tick;      // [3][kQ4MaxCtas]
   int* err;
+  unsigned long long timeout_ns;
 };
 
-// One CTA per (key-value head, batch row): the slots in tiles of 128; a thread
-// is a slot in the scores and a dimension in the output.
-__global__ void __launch_bounds__(128)
-    k_decode_attention_q4(const __grid_constant__ AttnQ4Params a) {
-  const int g = blockIdx.x, b = blockIdx.y, G = a.G, t = threadIdx.x;
-  const int pos = a.pos[b];
-  if (pos < 0) return;
-  if (pos >= a.S) {
-    if (t == 0) atomicExch(a.err, kDerrBadSlot);
-    return;
+__device__ __forceinline__ int q4_tiles(int pos, int S) {
+  return pos < 0 || pos >= S ? 0 : pos / kQ4Tile + 1;
+}
+
+// Two codes of a word, one in the low nibble of each half, as bf16 (code - 8):
+// 0x4300 | code is 128 + code, and 136 off it is exact.
+__device__ __forceinline__ uint32_t q4_pair(uint32_t m, int i) {
+  const uint32_t v = ((m >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+  const uint32_t c = 0x43084308u;
+  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&c));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// v = hi + lo, hi = bf16(v), lo = bf16(v - hi), two values a word
+__device__ __forceinline__ void q4_split(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  const __nv_bfloat162 l = __floats2bfloat162_rn(a - __low2float(h), b - __high2float(h));
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+__device__ __forceinline__ float q4_exp2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ unsigned q4_ticket(unsigned* p) {
+  unsigned old;
+  asm volatile("atom.add.acq_rel.gpu.u32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
+  return old;
+}
+
+// Where a warp's next tile lies: tile x of the CTA's range (counted from the
+// range's start) is tile x - at of (row b, head g), which has nt tiles.
+struct Q4Cursor {
+  int b, g, at, nt, pos;
+};
+
+__device__ __forceinline__ void q4_seek(const AttnQ4Params& a, Q4Cursor& c, int x) {
+  while (x >= c.at + c.nt) {
+    c.at += c.nt;
+    if (++c.g == a.nkv) {
+      c.g = 0;
+      do {
+        c.pos = a.pos[++c.b];
+        c.nt = q4_tiles(c.pos, a.S);
+      } while (c.nt == 0);
+    }
   }
-  __shared__ float qs[kQ4MaxG][kKvDim], sc[kQ4MaxG][kQ4Tile];
-  const size_t bg = (size_t)b * a.nkv + g;
-  unsigned char* kr = a.kc + bg * a.S * kKvRow;
-  unsigned char* vr = a.vc + bg * a.S * kKvRow;
-  if (t < 32) {
+}
+
+// Stage one tile: its cached rows by two bulk copies; in the sequence's last
+// tile the new row, quantised, goes to its place there and in the cache, and
+// the rows behind it become zeros (whatever the cache holds there).
+__device__ __forceinline__ void q4_stage(const AttnQ4Params& a, const Q4Cursor& c, int tile,
+                                         unsigned char* st, uint64_t* bar, int lane,
+                                         uint64_t pol) {
+  const int slot0 = tile * kQ4Tile, n = min(kQ4Tile, c.pos - slot0);  // cached rows
+  const size_t seg = (size_t)c.b * a.nkv + c.g, row0 = seg * a.S + slot0;
+  fence_proxy_async_smem();  // what the lanes read and wrote there before the copies
+  __syncwarp();
+  if (lane == 0) {
+    mbar_arrive_expect_tx(bar, 2u * n * kKvRow);
+    if (n > 0) {
+      bulk_copy_g2s(st, a.kc + row0 * kKvRow, n * kKvRow, bar, pol);
+      bulk_copy_g2s(st + kQ4Tile * kKvRow, a.vc + row0 * kKvRow, n * kKvRow, bar, pol);
+    }
+  }
+  if (n < kQ4Tile) {
+    const bool keys = lane < 16;
     float x[8];
-    const bool keys = t < 16;
-    load8<DT_F32>((keys ? a.k_new : a.v_new) + bg * kKvDim + (t & 15) * 8, x);
+    load8<DT_F32>((keys ? a.k_new : a.v_new) + seg * kKvDim + (lane & 15) * 8, x);
     uint32_t sz;
     const uint32_t w = quantize8(x, sz);
-    put_row((keys ? kr : vr) + (size_t)pos * kKvRow, w, sz, keys, true);
+    put_row(st + ((keys ? 0 : kQ4Tile) + n) * kKvRow, w, sz, keys, true);
+    put_row((keys ? a.kc : a.vc) + (row0 + n) * kKvRow, w, sz, keys, true);
+    uint4* z = reinterpret_cast<uint4*>(st + (keys ? 0 : kQ4Tile * kKvRow));
+    for (int i = (n + 1) * 5 + (lane & 15); i < kQ4Tile * 5; i += 16) z[i] = make_uint4(0, 0, 0, 0);
+    __syncwarp();
   }
-  for (int h = 0; h < G; ++h)
-    qs[h][t] = a.q[((size_t)b * a.nh + (size_t)g * G + h) * kKvDim + t] * a.scale;
-  __syncthreads();
-  float m[kQ4MaxG], l[kQ4MaxG], o[kQ4MaxG];
+}
+
+// O, L of n partial results for this thread's dimension and all heads; entry
+// i at src + i * step.  sm: 2 * 8 floats a warp's worth per entry batch.
+struct Q4Merged {
+  float O[kQ4MaxG], M[kQ4MaxG], L[kQ4MaxG];
+};
+
+__device__ __forceinline__ void q4_merge(const float* first, const float* rest, size_t step, int n,
+                                         int G, int t, Q4Merged& r) {
 #pragma unroll
-  for (int h = 0; h < kQ4MaxG; ++h) m[h] = -INFINITY, l[h] = 0.f, o[h] = 0.f;
-  const int unit = 4 * ((t & 31) >> 2) + (t >> 5), nib = 4 * (t & 3);
-  for (int j0 = 0; j0 <= pos; j0 += kQ4Tile) {
-    const int n = min(kQ4Tile, pos + 1 - j0);
-    __syncthreads();
-    if (t < n) {
-      const uint32_t* row = reinterpret_cast<const uint32_t*>(kr + (size_t)(j0 + t) * kKvRow);
-      float s[kQ4MaxG];
-#pragma unroll
-      for (int h = 0; h < kQ4MaxG; ++h) s[h] = 0.f;
-      for (int w = 0; w < 16; ++w) {
-        const uint32_t c = row[w], sz = row[16 + (w & 3)];
-        const int d0 = 32 * (w & 3) + 8 * (w >> 2);
-        for (int i = 0; i < 8; ++i) {
-          const float x = bf16lo(sz) * (float)((int)((c >> (4 * i)) & 15) - 8) + bf16hi(sz);
-#pragma unroll
-          for (int h = 0; h < kQ4MaxG; ++h)
-            if (h < G) s[h] = fmaf(x, qs[h][d0 + i], s[h]);
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < kQ4MaxG; ++h)
-        if (h < G) sc[h][t] = s[h];
-    }
-    __syncthreads();
+  for (int h = 0; h < kQ4MaxG; ++h) r.O[h] = 0.f, r.M[h] = -1e30f, r.L[h] = 0.f;
+  constexpr int kBatch = 4;
+  for (int i0 = 0; i0 < n; i0 += kBatch) {
 #pragma unroll
     for (int h = 0; h < kQ4MaxG; ++h) {
-      if (h >= G) continue;
-      float mx = m[h];
-      for (int j = 0; j < n; ++j) mx = fmaxf(mx, sc[h][j]);
-      const float f = expf(m[h] - mx);
-      m[h] = mx;
-      l[h] *= f;
-      o[h] *= f;
-    }
-    for (int j = 0; j < n; ++j) {
-      const unsigned char* row = vr + (size_t)(j0 + j) * kKvRow;
-      const uint32_t c = reinterpret_cast<const uint16_t*>(row)[unit];
-      const uint32_t sz = reinterpret_cast<const uint32_t*>(row)[16 + (t >> 5)];
-      const float x = bf16lo(sz) * (float)((int)((c >> nib) & 15) - 8) + bf16hi(sz);
+      if (h >= G) break;
+      float o[kBatch], m[kBatch], l[kBatch], M = r.M[h];
 #pragma unroll
-      for (int h = 0; h < kQ4MaxG; ++h) {
-        if (h >= G) continue;
-        const float p = expf(sc[h][j] - m[h]);
-        l[h] += p;
-        o[h] = fmaf(p, x, o[h]);
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = min(i0 + j, n - 1);
+        const float* e = (i == 0 ? first : rest + i * step) + (size_t)h * kQ4Part;
+        o[j] = __ldcg(e + t);
+        m[j] = __ldcg(e + kKvDim);
+        l[j] = __ldcg(e + kKvDim + 1);
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) M = fmaxf(M, m[j]);
+      const float f = q4_exp2(r.M[h] - M);
+      r.O[h] *= f;
+      r.L[h] *= f;
+      r.M[h] = M;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const float w = i0 + j < n ? q4_exp2(m[j] - M) : 0.f;
+        if (i0 + j < n) {
+          r.O[h] = fmaf(w, o[j], r.O[h]);
+          r.L[h] = fmaf(w, l[j], r.L[h]);
+        }
       }
     }
   }
-#pragma unroll
-  for (int h = 0; h < kQ4MaxG; ++h) {
-    if (h >= G) continue;
-    const size_t at = ((size_t)b * a.nh + (size_t)g * G + h) * kKvDim + t;
-    const float v = o[h] / l[h];
-    if (a.out_f32) a.out_f32[at] = v;
-    if (a.out_bf16) a.out_bf16[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+__device__ __forceinline__ void q4_write(const AttnQ4Params& a, int b, int g, int d, int h, float v) {
+  const size_t at = ((size_t)b * a.nh + (size_t)g * a.G + h) * kKvDim + d;
+  if (a.out_f32) a.out_f32[at] = v;
+  if (a.out_bf16) a.out_bf16[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+__global__ void __launch_bounds__(kQ4Threads, 3)
+    k_decode_attention_q4(const __grid_constant__ AttnQ4Params a) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ uint64_t full[kQ4Warps][kQ4Stages];
+  __shared__ float cm[kQ4Warps][kQ4MaxG], cl[kQ4Warps][kQ4MaxG];
+  __shared__ int last;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, G = a.G;
+  const int rg = lane >> 2, rt = lane & 3;  // row and column of the fragments
+
+  // the tiles of all rows and heads, cut into as many equal runs as there are
+  // CTAs; every warp finds the run's place by itself
+  long long total = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int p = b0 + lane < a.B ? a.pos[b0 + lane] : -1;
+    if (p >= a.S && blockIdx.x == 0 && warp == 0) atomicExch(a.err, kDerrBadSlot);
+    total += q4_tiles(p, a.S);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  total *= a.nkv;
+  const int per = (int)max((total + gridDim.x - 1) / gridDim.x, (long long)kQ4MinTiles);
+  const long long start = (long long)blockIdx.x * per;
+  const int run = (int)min((long long)per, total - start);
+  if (run <= 0) return;
+  Q4Cursor cur;
+  {
+    long long before = 0;
+    for (int b0 = 0;; b0 += 32) {
+      const int p = b0 + lane < a.B ? a.pos[b0 + lane] : -1;
+      const int nt = q4_tiles(p, a.S);
+      long long sum = (long long)nt * a.nkv;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += u;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, before + sum > start);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        cur.b = b0 + l;
+        cur.pos = __shfl_sync(0xffffffffu, p, l);
+        cur.nt = __shfl_sync(0xffffffffu, nt, l);
+        const long long in = start - before - (__shfl_sync(0xffffffffu, sum, l) -
+                                               (long long)cur.nt * a.nkv);
+        cur.g = (int)(in / cur.nt);
+        cur.at = -(int)(in % cur.nt);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+  }
+  unsigned char* ring = smem + warp * kQ4Stages * kQ4StageBytes;
+  float* comb = reinterpret_cast<float*>(smem + kQ4Ring);
+  if (lane == 0) {
+#pragma unroll
+    for (int s = 0; s < kQ4Stages; ++s) mbar_init(&full[warp][s], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  const uint64_t pol = l2_policy_evict_first();
+  Q4Cursor ic = cur;    // issue position
+  int xi = warp, ni = 0, nc = 0;
+  auto issue = [&]() {
+    if (xi < run) {
+      q4_seek(a, ic, xi);
+      q4_stage(a, ic, xi - ic.at, ring + ni * kQ4StageBytes, &full[warp][ni], lane, pol);
+      ni = ni + 1 == kQ4Stages ? 0 : ni + 1;
+    }
+    xi += kQ4Warps;
+  };
+#pragma unroll 1
+  for (int s = 0; s < kQ4Stages; ++s) issue();
+
+  int x = warp, x0 = 0;
+  uint32_t par = 0;
+  bool abort = false;
+  while (x0 < run) {  // one (row, head) at a time
+    q4_seek(a, cur, x0);
+    const int x1 = min(run, cur.at + cur.nt);
+    // the queries as the first product's A operand: head rg in rows rg (hi
+    // terms) and rg + 8 (lo terms); lane rt of a quad holds dimensions
+    // 32 g + 8 rt .. + 7, in the order of the key row's nibbles
+    uint32_t qf[8][4];
+    float qx[4];
+    {
+      const float* qr = a.q + ((size_t)cur.b * a.nh + (size_t)cur.g * G + (rg < G ? rg : 0)) * kKvDim;
+      const float z = rg < G ? a.scale : 0.f;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float v[8];
+        load8<DT_F32>(qr + 32 * g + 8 * rt, v);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[i] = rg < G ? v[i] * z : 0.f;
+          sum += v[i];
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        qx[g] = sum;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          q4_split(v[2 * s], v[2 * s + 4], qf[2 * g + s][0], qf[2 * g + s][1]);
+          q4_split(v[2 * s + 1], v[2 * s + 5], qf[2 * g + s][2], qf[2 * g + s][3]);
+        }
+      }
+    }
+    float o[16][4], zo[4] = {0.f, 0.f, 0.f, 0.f}, m = -1e30f, l = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+
+    for (; x < x1; x += kQ4Warps) {
+      const unsigned char* st = ring + nc * kQ4StageBytes;
+      const bool ok = abort || mbar_wait_bounded(&full[warp][nc], par, a.timeout_ns);
+      if (__any_sync(0xffffffffu, !ok) && !abort) {
+        abort = true;
+        if (lane == 0) atomicExch(a.err, (int)DERR_TIMEOUT);
+      }
+      if (!abort) {
+        // scores: head rg, slots 8 n + 2 rt + e
+        float s[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+        {
+          uint4 kw[2], ks[2][2];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            kw[n] = *reinterpret_cast<const uint4*>(st + (8 * n + rg) * kKvRow + 16 * rt);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              ks[n][e] = *reinterpret_cast<const uint4*>(st + (8 * n + 2 * rt + e) * kKvRow + kKvCodes);
+          }
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const uint32_t w = reinterpret_cast<const uint32_t*>(&kw[n])[g];
+              float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                mma_bf16_16816(c, qf[2 * g + k][0], qf[2 * g + k][1], qf[2 * g + k][2],
+                               qf[2 * g + k][3], q4_pair(w, 2 * k), q4_pair(w, 2 * k + 1));
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t sz = reinterpret_cast<const uint32_t*>(&ks[n][e])[g];
+                s[n][e] = fmaf(bf16lo(sz), c[e] + c[2 + e], fmaf(bf16hi(sz), qx[g], s[n][e]));
+              }
+            }
+        }
+        const int slot = (x - cur.at) * kQ4Tile + 2 * rt;
+        if (slot - 2 * rt + kQ4Tile > cur.pos + 1) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (slot + 8 * n + e > cur.pos) s[n][e] = -INFINITY;
+        }
+        float mx = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        if (__any_sync(0xffffffffu, mx > m + kQ4Lazy)) {
+          const float mn = fmaxf(m, mx), f = q4_exp2(m - mn);
+          m = mn;
+          l *= f;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) zo[g] *= f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][e] *= f;
+        }
+        float p[2][2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            p[n][e] = q4_exp2(s[n][e] - m);
+            l += p[n][e];
+          }
+        // output: the probabilities times each slot's scale enter as the A
+        // operand (hi rows and lo rows again), the codes as B: column rg is
+        // dimension 32 g + 4 rg + i
+        const unsigned char* sv = st + kQ4Tile * kKvRow;
+        uint2 vw[2][2];
+        uint4 vs[2][2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const unsigned char* r = sv + (8 * n + 2 * rt + e) * kKvRow;
+            vw[n][e] = *reinterpret_cast<const uint2*>(r + 8 * rg);
+            vs[n][e] = *reinterpret_cast<const uint4*>(r + kKvCodes);
+          }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          uint32_t ah[2], al[2], mm[2];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            float ps[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t sz = reinterpret_cast<const uint32_t*>(&vs[n][e])[g];
+              ps[e] = p[n][e] * bf16lo(sz);
+              zo[g] = fmaf(p[n][e], bf16hi(sz), zo[g]);
+            }
+            q4_split(ps[0], ps[1], ah[n], al[n]);
+            const uint32_t w0 = g < 2 ? vw[n][0].x : vw[n][0].y, w1 = g < 2 ? vw[n][1].x : vw[n][1].y;
+            mm[n] = __byte_perm(w0, w1, g & 1 ? 0x7632 : 0x5410);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mma_bf16_16816(o[4 * g + i], ah[0], al[0], ah[1], al[1], q4_pair(mm[0], i),
+                           q4_pair(mm[1], i));
+        }
+      }
+      nc = nc + 1 == kQ4Stages ? 0 : nc + 1;
+      par ^= nc == 0;
+      issue();
+    }
+
+    // the four warps' results, then this CTA's: dimensions 32 g + 8 rt .. + 7
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      zo[g] += __shfl_xor_sync(0xffffffffu, zo[g], 1);
+      zo[g] += __shfl_xor_sync(0xffffffffu, zo[g], 2);
+    }
+    if (rt == 0) cm[warp][rg] = m, cl[warp][rg] = l;
+    float* cw = comb + ((size_t)warp * kQ4MaxG + rg) * kKvDim + 8 * rt;
+    if (rg < G) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float4*>(cw + 32 * g + 4 * e) =
+              make_float4(o[4 * g][e] + o[4 * g][2 + e] + zo[g],
+                          o[4 * g + 1][e] + o[4 * g + 1][2 + e] + zo[g],
+                          o[4 * g + 2][e] + o[4 * g + 2][2 + e] + zo[g],
+                          o[4 * g + 3][e] + o[4 * g + 3][2 + e] + zo[g]);
+    }
+    __syncthreads();
+    const long long seg0 = start + cur.at;  // the segment's first tile among all
+    const int c0 = (int)(seg0 / per), n = (int)((seg0 + cur.nt - 1) / per) - c0 + 1;
+    const int me = blockIdx.x - c0;
+    const size_t slot = (size_t)2 * G * kQ4Part;  // floats of a CTA's two partials
+    float* mine = a.part + (size_t)blockIdx.x * slot + (me == 0 ? slot / 2 : 0);
+#pragma unroll
+    for (int h = 0; h < kQ4MaxG; ++h) {
+      if (h >= G) break;
+      float M = cm[0][h], O = 0.f, L = 0.f;
+#pragma unroll
+      for (int w = 1; w < kQ4Warps; ++w) M = fmaxf(M, cm[w][h]);
+#pragma unroll
+      for (int w = 0; w < kQ4Warps; ++w) {
+        const float f = q4_exp2(cm[w][h] - M);
+        O = fmaf(f, comb[((size_t)w * kQ4MaxG + h) * kKvDim + t], O);
+        L = fmaf(f, cl[w][h], L);
+      }
+      if (n == 1) {
+        q4_write(a, cur.b, cur.g, t, h, O / L);
+      } else {
+        mine[h * kQ4Part + t] = O;
+        if (t == 0) mine[h * kQ4Part + kKvDim] = M, mine[h * kQ4Part + kKvDim + 1] = L;
+      }
+    }
+    if (n > 1) {
+      // the last CTA of each 16 merges them into the first one's place, the
+      // last of the groups merges the groups
+      const int grp = me / kQ4Merge, in = min(kQ4Merge, n - grp * kQ4Merge);
+      const int groups = (n + kQ4Merge - 1) / kQ4Merge;
+      const float* base = a.part + (size_t)c0 * slot;  // CTA c0's entry is its second one
+      float* first = const_cast<float*>(base) + (grp ? (size_t)grp * kQ4Merge * slot : slot / 2);
+      __syncthreads();
+      if (t == 0) {
+        unsigned* tk = a.tick + (grp ? kQ4MaxCtas : 0) + c0 + grp * kQ4Merge;
+        last = q4_ticket(tk) == (unsigned)(in - 1);
+        if (last) *tk = 0;
+      }
+      __syncthreads();
+      if (last) {
+        Q4Merged r;
+        q4_merge(first, base + (size_t)grp * kQ4Merge * slot, slot, in, G, t, r);
+        if (groups > 1) {
+          __syncthreads();
+#pragma unroll
+          for (int h = 0; h < kQ4MaxG; ++h) {
+            if (h >= G) break;
+            first[h * kQ4Part + t] = r.O[h];
+            if (t == 0) first[h * kQ4Part + kKvDim] = r.M[h], first[h * kQ4Part + kKvDim + 1] = r.L[h];
+          }
+          __syncthreads();
+          if (t == 0) {
+            unsigned* tk = a.tick + 2 * kQ4MaxCtas + c0;
+            last = q4_ticket(tk) == (unsigned)(groups - 1);
+            if (last) *tk = 0;
+          }
+          __syncthreads();
+          if (last) q4_merge(base + slot / 2, base, kQ4Merge * slot, groups, G, t, r);
+        }
+        if (last) {
+#pragma unroll
+          for (int h = 0; h < kQ4MaxG; ++h) {
+            if (h >= G) break;
+            q4_write(a, cur.b, cur.g, t, h, r.O[h] / r.L[h]);
+          }
+        }
+      }
+    }
+    __syncthreads();  // cm, cl and comb are free again
+    x0 = x1;
+  }
+}
+
+// Resident CTAs of the device: the grid, set up once per device.
+static int q4_grid(cudaError_t* err) {
+  constexpr int kMaxDev = 64;
+  static std::mutex mu;
+  static int grid[kMaxDev] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= kMaxDev) {
+    *err = e != cudaSuccess ? e : cudaErrorInvalidDevice;
+    return 0;
+  }
+  std::lock_guard<std::mutex> lk(mu);
+  if (!grid[dev]) {
+    int sms = 0, per_sm = 0;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k_decode_attention_q4, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kQ4Smem);
+    if (e == cudaSuccess)
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_decode_attention_q4, kQ4Threads,
+                                                        kQ4Smem);
+    if (e != cudaSuccess || per_sm < 1) {
+      *err = e != cudaSuccess ? e : cudaErrorInvalidConfiguration;
+      return 0;
+    }
+    grid[dev] = sms * per_sm < kQ4MaxCtas ? sms * per_sm : kQ4MaxCtas;
+  }
+  return grid[dev];
+}
+
+static size_t q4_workspace(int nh, int nkv) {
+  return 3 * kQ4MaxCtas * 4 + (size_t)kQ4MaxCtas * 2 * (nh / nkv) * kQ4Part * 4;
 }
 
 static bool q4_shape_ok(int B, int nh, int nkv, int d, int S) {
@@ -130,7 +539,7 @@ extern "C" {
 size_t ws_attention_q4_workspace_bytes(int B, int n_heads, int n_kv_heads, int head_dim,
                                        int s_max) {
   if (!q4_shape_ok(B, n_heads, n_kv_heads, head_dim, s_max)) return 0;
-  return 256;
+  return q4_workspace(n_heads, n_kv_heads);
 }
 
 ws_status ws_decode_attention_q4(const float *q, const float *k_new, const float *v_new,
@@ -166,20 +575,30 @@ ws_status ws_decode_attention_q4(const float *q, const float *k_new, const float
   a.kc = static_cast<unsigned char*>(k_cache);
   a.vc = static_cast<unsigned char*>(v_cache);
   a.pos = pos;
+  a.B = B;
   a.out_f32 = out_f32;
   a.out_bf16 = static_cast<uint16_t*>(out_bf16);
   a.nh = n_heads;
   a.nkv = n_kv_heads;
   a.S = s_max;
   a.G = n_heads / n_kv_heads;
-  a.scale = 1.0f / sqrtf((float)kKvDim);
+  a.scale = (float)(1.4426950408889634 / sqrt((double)kKvDim));
+  a.tick = static_cast<unsigned*>(workspace);
+  a.part = reinterpret_cast<float*>(a.tick + 3 * kQ4MaxCtas);
+  a.timeout_ns = tuning().timeout_ns;
   a.err = device_error_ptr();
   if (!a.err) {
     set_error("device error flag unavailable");
     return WS_ERR_CUDA;
   }
-  k_decode_attention_q4<<<dim3(n_kv_heads, B), 128, 0, (cudaStream_t)stream>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  cudaError_t e = cudaSuccess;
+  const int grid = q4_grid(&e);
+  if (!grid) {
+    set_error("4-bit decode attention setup failed: %s", cudaGetErrorString(e));
+    return WS_ERR_CUDA;
+  }
+  k_decode_attention_q4<<<grid, kQ4Threads, kQ4Smem, (cudaStream_t)stream>>>(a);
+  e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("launch failed: %s", cudaGetErrorString(e));
     return WS_ERR_CUDA;
