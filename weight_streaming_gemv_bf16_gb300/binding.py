@@ -204,8 +204,14 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# the current stream's handle without a Stream object (0.1 us against 3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream

@@ -14,15 +14,15 @@ namespace ws {
 
 constexpr int kQ4MaxG = 8;       // query heads per key-value head (half the MMA's 16 rows)
 constexpr int kQ4MaxB = 1024;
-constexpr int kQ4Tile = 16;      // slots per tile
+constexpr int kQ4Tile = 32;      // slots per tile: four of the products' 8 columns
 constexpr int kQ4Warps = 4;
 constexpr int kQ4Threads = kQ4Warps * 32;
-constexpr int kQ4Stages = 4;     // ring stages per warp
+constexpr int kQ4Stages = 2;     // ring stages per warp
 constexpr int kQ4StageBytes = 2 * kQ4Tile * kKvRow;  // keys, then values
 constexpr int kQ4MaxCtas = 1024;
-constexpr int kQ4MinTiles = 2 * kQ4Warps;            // tiles a CTA takes at least
+constexpr int kQ4MinTiles = 1 * kQ4Warps;            // tiles a CTA takes at least
 constexpr int kQ4Merge = 16;                         // partial results merged in one go
-constexpr int kQ4Part = kKvDim + 2;                  // one partial result: acc[128], max, sum
+constexpr int kQ4Part = kKvDim + 4;                  // one partial result: acc[128], max, sum, two unused
 constexpr int kQ4Ring = kQ4Warps * kQ4Stages * kQ4StageBytes;
 constexpr int kQ4Smem = kQ4Ring + kQ4Warps * kQ4MaxG * kKvDim * 4;
 // the running maximum follows the tile's only when that is 2^8 above it
@@ -63,7 +63,7 @@ __device__ __forceinline__ uint32_t q4_pair(uint32_t m, int i) {
 __device__ __forceinline__ void q4_split(float a, float b, uint32_t& hi, uint32_t& lo) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   hi = *reinterpret_cast<const uint32_t*>(&h);
-  const __nv_bfloat162 l = __floats2bfloat162_rn(a - __low2float(h), b - __high2float(h));
+  const __nv_bfloat162 l = __floats2bfloat162_rn(a - bf16lo(hi), b - bf16hi(hi));
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
@@ -98,83 +98,115 @@ __device__ __forceinline__ void q4_seek(const AttnQ4Params& a, Q4Cursor& c, int 
   }
 }
 
-// Stage one tile: its cached rows by two bulk copies; in the sequence's last
-// tile the new row, quantised, goes to its place there and in the cache, and
-// the rows behind it become zeros (whatever the cache holds there).
-__device__ __forceinline__ void q4_stage(const AttnQ4Params& a, const Q4Cursor& c, int tile,
-                                         unsigned char* st, uint64_t* bar, int lane,
-                                         uint64_t pol) {
-  const int slot0 = tile * kQ4Tile, n = min(kQ4Tile, c.pos - slot0);  // cached rows
-  const size_t seg = (size_t)c.b * a.nkv + c.g, row0 = seg * a.S + slot0;
-  fence_proxy_async_smem();  // what the lanes read and wrote there before the copies
-  __syncwarp();
+// The sequence's last tile: its n cached rows by bulk copies, then the new row,
+// quantised, to its place there and in the cache, and zeros for the rows behind
+// it (whatever the cache holds there).
+__device__ __noinline__ void q4_stage_last(const AttnQ4Params& a, size_t seg, int n,
+                                           unsigned char* kr, unsigned char* vr, unsigned char* st,
+                                           uint64_t* bar, int lane, uint64_t pol) {
   if (lane == 0) {
     mbar_arrive_expect_tx(bar, 2u * n * kKvRow);
     if (n > 0) {
-      bulk_copy_g2s(st, a.kc + row0 * kKvRow, n * kKvRow, bar, pol);
-      bulk_copy_g2s(st + kQ4Tile * kKvRow, a.vc + row0 * kKvRow, n * kKvRow, bar, pol);
+      bulk_copy_g2s(st, kr, n * kKvRow, bar, pol);
+      bulk_copy_g2s(st + kQ4Tile * kKvRow, vr, n * kKvRow, bar, pol);
     }
   }
-  if (n < kQ4Tile) {
-    const bool keys = lane < 16;
-    float x[8];
-    load8<DT_F32>((keys ? a.k_new : a.v_new) + seg * kKvDim + (lane & 15) * 8, x);
-    uint32_t sz;
-    const uint32_t w = quantize8(x, sz);
-    put_row(st + ((keys ? 0 : kQ4Tile) + n) * kKvRow, w, sz, keys, true);
-    put_row((keys ? a.kc : a.vc) + (row0 + n) * kKvRow, w, sz, keys, true);
-    uint4* z = reinterpret_cast<uint4*>(st + (keys ? 0 : kQ4Tile * kKvRow));
-    for (int i = (n + 1) * 5 + (lane & 15); i < kQ4Tile * 5; i += 16) z[i] = make_uint4(0, 0, 0, 0);
-    __syncwarp();
-  }
+  const bool keys = lane < 16;
+  float x[8];
+  load8<DT_F32>((keys ? a.k_new : a.v_new) + seg * kKvDim + (lane & 15) * 8, x);
+  uint32_t sz;
+  const uint32_t w = quantize8(x, sz);
+  put_row(st + ((keys ? 0 : kQ4Tile) + n) * kKvRow, w, sz, keys, true);
+  put_row((keys ? kr : vr) + n * kKvRow, w, sz, keys, true);
+  uint4* z = reinterpret_cast<uint4*>(st + (keys ? 0 : kQ4Tile * kKvRow));
+  for (int i = (n + 1) * 5 + (lane & 15); i < kQ4Tile * 5; i += 16) z[i] = make_uint4(0, 0, 0, 0);
+  __syncwarp();
 }
 
-// O, L of n partial results for this thread's dimension and all heads; entry
-// i at src + i * step.  sm: 2 * 8 floats a warp's worth per entry batch.
-struct Q4Merged {
-  float O[kQ4MaxG], M[kQ4MaxG], L[kQ4MaxG];
-};
+// Two fp32 values a register pair: one instruction for both.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
 
+// Merge of n partial results (entry i at rest + i * step, entry 0 at first) for
+// head h by one warp, four dimensions a lane: M = max m, L = sum 2^(m - M) l,
+// O = sum 2^(m - M) acc.  A batch's loads are all in flight together.
 __device__ __forceinline__ void q4_merge(const float* first, const float* rest, size_t step, int n,
-                                         int G, int t, Q4Merged& r) {
+                                         int h, int lane, float4& O, float& M, float& L) {
+  O = make_float4(0.f, 0.f, 0.f, 0.f);
+  M = -1e30f;
+  L = 0.f;
+  for (int i0 = 0; i0 < n; i0 += kQ4Merge) {
+    float4 x[kQ4Merge];
 #pragma unroll
-  for (int h = 0; h < kQ4MaxG; ++h) r.O[h] = 0.f, r.M[h] = -1e30f, r.L[h] = 0.f;
-  constexpr int kBatch = 4;
-  for (int i0 = 0; i0 < n; i0 += kBatch) {
+    for (int j = 0; j < kQ4Merge; ++j) {
+      const int i = min(i0 + j, n - 1);
+      const float* e = (i == 0 ? first : rest + i * step) + (size_t)h * kQ4Part;
+      x[j] = __ldcg(reinterpret_cast<const float4*>(e) + lane);
+    }
+    const int i = min(i0 + (lane & (kQ4Merge - 1)), n - 1);
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(
+        (i == 0 ? first : rest + i * step) + (size_t)h * kQ4Part + kKvDim));
+    float mx = ml.x;
 #pragma unroll
-    for (int h = 0; h < kQ4MaxG; ++h) {
-      if (h >= G) break;
-      float o[kBatch], m[kBatch], l[kBatch], M = r.M[h];
+    for (int o = kQ4Merge / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    mx = fmaxf(mx, M);
+    const float f = q4_exp2(M - mx);
+    M = mx;
+    float w = i0 + (lane & (kQ4Merge - 1)) < n ? q4_exp2(ml.x - mx) : 0.f;
+    float lw = w * ml.y;
+    if (i0 + (lane & (kQ4Merge - 1)) >= n) lw = 0.f;
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int i = min(i0 + j, n - 1);
-        const float* e = (i == 0 ? first : rest + i * step) + (size_t)h * kQ4Part;
-        o[j] = __ldcg(e + t);
-        m[j] = __ldcg(e + kKvDim);
-        l[j] = __ldcg(e + kKvDim + 1);
-      }
+    for (int o = kQ4Merge / 2; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+    L = fmaf(L, f, lw);
+    O.x *= f, O.y *= f, O.z *= f, O.w *= f;
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) M = fmaxf(M, m[j]);
-      const float f = q4_exp2(r.M[h] - M);
-      r.O[h] *= f;
-      r.L[h] *= f;
-      r.M[h] = M;
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const float w = i0 + j < n ? q4_exp2(m[j] - M) : 0.f;
-        if (i0 + j < n) {
-          r.O[h] = fmaf(w, o[j], r.O[h]);
-          r.L[h] = fmaf(w, l[j], r.L[h]);
-        }
+    for (int j = 0; j < kQ4Merge; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      if (i0 + j < n) {
+        O.x = fmaf(wj, x[j].x, O.x);
+        O.y = fmaf(wj, x[j].y, O.y);
+        O.z = fmaf(wj, x[j].z, O.z);
+        O.w = fmaf(wj, x[j].w, O.w);
       }
     }
   }
 }
 
-__device__ __forceinline__ void q4_write(const AttnQ4Params& a, int b, int g, int d, int h, float v) {
-  const size_t at = ((size_t)b * a.nh + (size_t)g * a.G + h) * kKvDim + d;
-  if (a.out_f32) a.out_f32[at] = v;
-  if (a.out_bf16) a.out_bf16[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+// out = O / L, four dimensions a lane
+__device__ __forceinline__ void q4_write(const AttnQ4Params& a, int b, int g, int lane, int h,
+                                         float4 O, float L) {
+  const size_t at = ((size_t)b * a.nh + (size_t)g * a.G + h) * kKvDim + 4 * lane;
+  O.x /= L, O.y /= L, O.z /= L, O.w /= L;
+  if (a.out_f32) *reinterpret_cast<float4*>(a.out_f32 + at) = O;
+  if (a.out_bf16) {
+    const __nv_bfloat162 u = __floats2bfloat162_rn(O.x, O.y), v = __floats2bfloat162_rn(O.z, O.w);
+    *reinterpret_cast<uint2*>(a.out_bf16 + at) = make_uint2(
+        *reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
+  }
+}
+
+__device__ __forceinline__ void q4_put(float* e, int lane, float4 O, float M, float L) {
+  reinterpret_cast<float4*>(e)[lane] = O;
+  if (lane == 0) *reinterpret_cast<float2*>(e + kKvDim) = make_float2(M, L);
 }
 
 __global__ void __launch_bounds__(kQ4Threads, 3)
@@ -188,29 +220,28 @@ __global__ void __launch_bounds__(kQ4Threads, 3)
 
   // the tiles of all rows and heads, cut into as many equal runs as there are
   // CTAs; every warp finds the run's place by itself
-  long long total = 0;
+  // (fewer than 2^31 of them: a tile is 5120 bytes of cache)
+  int total = 0, p0 = -1;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int p = b0 + lane < a.B ? a.pos[b0 + lane] : -1;
+    if (b0 == 0) p0 = p;
     if (p >= a.S && blockIdx.x == 0 && warp == 0) atomicExch(a.err, kDerrBadSlot);
     total += q4_tiles(p, a.S);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  total *= a.nkv;
-  const int per = (int)max((total + gridDim.x - 1) / gridDim.x, (long long)kQ4MinTiles);
-  const long long start = (long long)blockIdx.x * per;
-  const int run = (int)min((long long)per, total - start);
+  total = __reduce_add_sync(0xffffffffu, total) * a.nkv;
+  const int per = max((int)((total + gridDim.x - 1) / gridDim.x), kQ4MinTiles);
+  const int start = blockIdx.x * per, run = min(per, total - start);
   if (run <= 0) return;
   Q4Cursor cur;
   {
-    long long before = 0;
+    int before = 0;
     for (int b0 = 0;; b0 += 32) {
-      const int p = b0 + lane < a.B ? a.pos[b0 + lane] : -1;
+      const int p = b0 == 0 ? p0 : b0 + lane < a.B ? a.pos[b0 + lane] : -1;
       const int nt = q4_tiles(p, a.S);
-      long long sum = (long long)nt * a.nkv;
+      int sum = nt * a.nkv;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, sum, o);
+        const int u = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += u;
       }
       const unsigned hit = __ballot_sync(0xffffffffu, before + sum > start);
@@ -219,10 +250,9 @@ __global__ void __launch_bounds__(kQ4Threads, 3)
         cur.b = b0 + l;
         cur.pos = __shfl_sync(0xffffffffu, p, l);
         cur.nt = __shfl_sync(0xffffffffu, nt, l);
-        const long long in = start - before - (__shfl_sync(0xffffffffu, sum, l) -
-                                               (long long)cur.nt * a.nkv);
-        cur.g = (int)(in / cur.nt);
-        cur.at = -(int)(in % cur.nt);
+        const int in = start - before - (__shfl_sync(0xffffffffu, sum, l) - cur.nt * a.nkv);
+        cur.g = in / cur.nt;
+        cur.at = -(in % cur.nt);
         break;
       }
       before += __shfl_sync(0xffffffffu, sum, 31);
@@ -237,18 +267,41 @@ __global__ void __launch_bounds__(kQ4Threads, 3)
   }
   __syncwarp();
   const uint64_t pol = l2_policy_evict_first();
-  Q4Cursor ic = cur;    // issue position
+  // the next tile to stage: its segment, and its rows' addresses there
+  Q4Cursor ic = cur;
   int xi = warp, ni = 0, nc = 0;
+  unsigned char *ikr = nullptr, *ivr = nullptr;
+  int ilast = -1;  // the last tile of the segment, counted as x
   auto issue = [&]() {
     if (xi < run) {
-      q4_seek(a, ic, xi);
-      q4_stage(a, ic, xi - ic.at, ring + ni * kQ4StageBytes, &full[warp][ni], lane, pol);
-      ni = ni + 1 == kQ4Stages ? 0 : ni + 1;
+      if (xi > ilast) {
+        q4_seek(a, ic, xi);
+        ilast = ic.at + ic.nt - 1;
+        const size_t row = ((size_t)ic.b * a.nkv + ic.g) * a.S + (size_t)(xi - ic.at) * kQ4Tile;
+        ikr = a.kc + row * kKvRow;
+        ivr = a.vc + row * kKvRow;
+      }
+      unsigned char* st = ring + ni * kQ4StageBytes;
+      uint64_t* bar = &full[warp][ni];
+      fence_proxy_async_smem();  // what the lanes read and wrote there before the copies
+      __syncwarp();
+      if (xi == ilast) {
+        q4_stage_last(a, (size_t)ic.b * a.nkv + ic.g, ic.pos - (xi - ic.at) * kQ4Tile, ikr, ivr, st,
+                      bar, lane, pol);
+      } else if (lane == 0) {
+        mbar_arrive_expect_tx(bar, kQ4StageBytes);
+        bulk_copy_g2s(st, ikr, kQ4Tile * kKvRow, bar, pol);
+        bulk_copy_g2s(st + kQ4Tile * kKvRow, ivr, kQ4Tile * kKvRow, bar, pol);
+      }
+      ni ^= 1;
+      ikr += kQ4Warps * kQ4Tile * kKvRow;
+      ivr += kQ4Warps * kQ4Tile * kKvRow;
     }
     xi += kQ4Warps;
   };
-#pragma unroll 1
-  for (int s = 0; s < kQ4Stages; ++s) issue();
+  static_assert(kQ4Stages == 2, "stage indices flip");
+  issue();
+  issue();
 
   int x = warp, x0 = 0;
   uint32_t par = 0;
@@ -258,12 +311,12 @@ __global__ void __launch_bounds__(kQ4Threads, 3)
     const int x1 = min(run, cur.at + cur.nt);
     // the queries as the first product's A operand: head rg in rows rg (hi
     // terms) and rg + 8 (lo terms); lane rt of a quad holds dimensions
-    // 32 g + 8 rt .. + 7, in the order of the key row's nibbles
-    uint32_t qf[8][4];
-    float qx[4];
+    // 32 g + 8 rt .. + 7, in the order of the key row's nibbles.  qz: their
+    // sums per group, the operand against the zeros (k = group)
+    uint32_t qf[8][4], qz[2];
     {
       const float* qr = a.q + ((size_t)cur.b * a.nh + (size_t)cur.g * G + (rg < G ? rg : 0)) * kKvDim;
-      const float z = rg < G ? a.scale : 0.f;
+      float sums[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         float v[8];
@@ -271,20 +324,26 @@ __global__ void __launch_bounds__(kQ4Threads, 3)
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          v[i] = rg < G ? v[i] * z : 0.f;
+          v[i] = rg < G ? v[i] * a.scale : 0.f;
           sum += v[i];
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        qx[g] = sum;
+        sums[g] = sum;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           q4_split(v[2 * s], v[2 * s + 4], qf[2 * g + s][0], qf[2 * g + s][1]);
           q4_split(v[2 * s + 1], v[2 * s + 5], qf[2 * g + s][2], qf[2 * g + s][3]);
         }
       }
+      q4_split(rt == 0 ? sums[0] : rt == 1 ? sums[2] : 0.f, rt == 0 ? sums[1] : rt == 1 ? sums[3] : 0.f,
+               qz[0], qz[1]);
     }
-    float o[16][4], zo[4] = {0.f, 0.f, 0.f, 0.f}, m = -1e30f, l = 0.f;
+    const uint32_t zmask = rt < 2 ? 0xffffffffu : 0u;
+    float o[16][4], m = -1e30f;
+    float2 l = make_float2(0.f, 0.f), zo[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) zo[g] = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < 16; ++i)
 #pragma unroll
@@ -292,120 +351,122 @@ __global__ void __launch_bounds__(kQ4Threads, 3)
 
     for (; x < x1; x += kQ4Warps) {
       const unsigned char* st = ring + nc * kQ4StageBytes;
-      const bool ok = abort || mbar_wait_bounded(&full[warp][nc], par, a.timeout_ns);
-      if (__any_sync(0xffffffffu, !ok) && !abort) {
-        abort = true;
-        if (lane == 0) atomicExch(a.err, (int)DERR_TIMEOUT);
+      bool ok = abort || mbar_try_wait(&full[warp][nc], par);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = ok || mbar_wait_bounded(&full[warp][nc], par, a.timeout_ns);
+        if (__any_sync(0xffffffffu, !ok)) {
+          abort = true;
+          if (lane == 0) atomicExch(a.err, (int)DERR_TIMEOUT);
+        }
       }
       if (!abort) {
         // scores: head rg, slots 8 n + 2 rt + e
-        float s[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-        {
-          uint4 kw[2], ks[2][2];
+        float2 s[4];
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            kw[n] = *reinterpret_cast<const uint4*>(st + (8 * n + rg) * kKvRow + 16 * rt);
+        for (int n = 0; n < 4; ++n) {
+          const unsigned char* kr = st + (8 * n + rg) * kKvRow;
+          const uint4 kw = *reinterpret_cast<const uint4*>(kr + 16 * rt);
+          const uint2 kz = *reinterpret_cast<const uint2*>(kr + kKvCodes + 8 * (rt & 1));
+          const unsigned char* ksp = st + (8 * n + 2 * rt) * kKvRow + kKvCodes;
+          const uint4 ks0 = *reinterpret_cast<const uint4*>(ksp);
+          const uint4 ks1 = *reinterpret_cast<const uint4*>(ksp + kKvRow);
+          float cz[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_bf16_16816(cz, qz[0], qz[1], 0u, 0u, __byte_perm(kz.x, kz.y, 0x7632) & zmask, 0u);
+          s[n] = add2(make_float2(cz[0], cz[1]), make_float2(cz[2], cz[3]));
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              ks[n][e] = *reinterpret_cast<const uint4*>(st + (8 * n + 2 * rt + e) * kKvRow + kKvCodes);
+          for (int g = 0; g < 4; ++g) {
+            const uint32_t w = reinterpret_cast<const uint32_t*>(&kw)[g];
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              mma_bf16_16816(c, qf[2 * g + k][0], qf[2 * g + k][1], qf[2 * g + k][2],
+                             qf[2 * g + k][3], q4_pair(w, 2 * k), q4_pair(w, 2 * k + 1));
+            s[n] = fma2(make_float2(bf16lo(reinterpret_cast<const uint32_t*>(&ks0)[g]),
+                                    bf16lo(reinterpret_cast<const uint32_t*>(&ks1)[g])),
+                        add2(make_float2(c[0], c[1]), make_float2(c[2], c[3])), s[n]);
           }
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const uint32_t w = reinterpret_cast<const uint32_t*>(&kw[n])[g];
-              float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-                mma_bf16_16816(c, qf[2 * g + k][0], qf[2 * g + k][1], qf[2 * g + k][2],
-                               qf[2 * g + k][3], q4_pair(w, 2 * k), q4_pair(w, 2 * k + 1));
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t sz = reinterpret_cast<const uint32_t*>(&ks[n][e])[g];
-                s[n][e] = fmaf(bf16lo(sz), c[e] + c[2 + e], fmaf(bf16hi(sz), qx[g], s[n][e]));
-              }
-            }
         }
-        const int slot = (x - cur.at) * kQ4Tile + 2 * rt;
-        if (slot - 2 * rt + kQ4Tile > cur.pos + 1) {
+        if ((x - cur.at + 1) * kQ4Tile > cur.pos + 1) {
+          const int slot = (x - cur.at) * kQ4Tile + 2 * rt;
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (slot + 8 * n + e > cur.pos) s[n][e] = -INFINITY;
+          for (int n = 0; n < 4; ++n) {
+            if (slot + 8 * n > cur.pos) s[n].x = -INFINITY;
+            if (slot + 8 * n + 1 > cur.pos) s[n].y = -INFINITY;
+          }
         }
-        float mx = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        float mx = fmaxf(fmaxf(fmaxf(s[0].x, s[0].y), fmaxf(s[1].x, s[1].y)),
+                         fmaxf(fmaxf(s[2].x, s[2].y), fmaxf(s[3].x, s[3].y)));
         if (__any_sync(0xffffffffu, mx > m + kQ4Lazy)) {
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           const float mn = fmaxf(m, mx), f = q4_exp2(m - mn);
           m = mn;
-          l *= f;
+          l.x *= f, l.y *= f;
 #pragma unroll
-          for (int g = 0; g < 4; ++g) zo[g] *= f;
+          for (int g = 0; g < 4; ++g) zo[g].x *= f, zo[g].y *= f;
 #pragma unroll
           for (int i = 0; i < 16; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][e] *= f;
         }
-        float p[2][2];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            p[n][e] = q4_exp2(s[n][e] - m);
-            l += p[n][e];
-          }
+        for (int n = 0; n < 4; ++n) {
+          s[n].x = q4_exp2(s[n].x - m);
+          s[n].y = q4_exp2(s[n].y - m);
+          l = add2(l, s[n]);
+        }
         // output: the probabilities times each slot's scale enter as the A
         // operand (hi rows and lo rows again), the codes as B: column rg is
         // dimension 32 g + 4 rg + i
-        const unsigned char* sv = st + kQ4Tile * kKvRow;
-        uint2 vw[2][2];
-        uint4 vs[2][2];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int u = 0; u < 2; ++u) {
+          const unsigned char* sv = st + (kQ4Tile + 16 * u + 2 * rt) * kKvRow;
+          uint2 vw[2][2];
+          uint4 vs[2][2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const unsigned char* r = sv + (8 * n + 2 * rt + e) * kKvRow;
-            vw[n][e] = *reinterpret_cast<const uint2*>(r + 8 * rg);
-            vs[n][e] = *reinterpret_cast<const uint4*>(r + kKvCodes);
-          }
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          uint32_t ah[2], al[2], mm[2];
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            float ps[2];
+          for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const uint32_t sz = reinterpret_cast<const uint32_t*>(&vs[n][e])[g];
-              ps[e] = p[n][e] * bf16lo(sz);
-              zo[g] = fmaf(p[n][e], bf16hi(sz), zo[g]);
+              const unsigned char* r = sv + (8 * n + e) * kKvRow;
+              vw[n][e] = *reinterpret_cast<const uint2*>(r + 8 * rg);
+              vs[n][e] = *reinterpret_cast<const uint4*>(r + kKvCodes);
             }
-            q4_split(ps[0], ps[1], ah[n], al[n]);
-            const uint32_t w0 = g < 2 ? vw[n][0].x : vw[n][0].y, w1 = g < 2 ? vw[n][1].x : vw[n][1].y;
-            mm[n] = __byte_perm(w0, w1, g & 1 ? 0x7632 : 0x5410);
-          }
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma_bf16_16816(o[4 * g + i], ah[0], al[0], ah[1], al[1], q4_pair(mm[0], i),
-                           q4_pair(mm[1], i));
+          for (int g = 0; g < 4; ++g) {
+            uint32_t ah[2], al[2], mm[2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const uint32_t z0 = reinterpret_cast<const uint32_t*>(&vs[n][0])[g];
+              const uint32_t z1 = reinterpret_cast<const uint32_t*>(&vs[n][1])[g];
+              const float2 ps = mul2(s[2 * u + n], make_float2(bf16lo(z0), bf16lo(z1)));
+              zo[g] = fma2(s[2 * u + n], make_float2(bf16hi(z0), bf16hi(z1)), zo[g]);
+              q4_split(ps.x, ps.y, ah[n], al[n]);
+              const uint32_t w0 = g < 2 ? vw[n][0].x : vw[n][0].y, w1 = g < 2 ? vw[n][1].x : vw[n][1].y;
+              mm[n] = __byte_perm(w0, w1, g & 1 ? 0x7632 : 0x5410);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma_bf16_16816(o[4 * g + i], ah[0], al[0], ah[1], al[1], q4_pair(mm[0], i),
+                             q4_pair(mm[1], i));
+          }
         }
       }
-      nc = nc + 1 == kQ4Stages ? 0 : nc + 1;
+      nc ^= 1;
       par ^= nc == 0;
       issue();
     }
 
     // the four warps' results, then this CTA's: dimensions 32 g + 8 rt .. + 7
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    float lsum = l.x + l.y, zs[4];
+    lsum += __shfl_xor_sync(0xffffffffu, lsum, 1);
+    lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      zo[g] += __shfl_xor_sync(0xffffffffu, zo[g], 1);
-      zo[g] += __shfl_xor_sync(0xffffffffu, zo[g], 2);
+      zs[g] = zo[g].x + zo[g].y;
+      zs[g] += __shfl_xor_sync(0xffffffffu, zs[g], 1);
+      zs[g] += __shfl_xor_sync(0xffffffffu, zs[g], 2);
     }
-    if (rt == 0) cm[warp][rg] = m, cl[warp][rg] = l;
+    if (rt == 0) cm[warp][rg] = m, cl[warp][rg] = lsum;
     float* cw = comb + ((size_t)warp * kQ4MaxG + rg) * kKvDim + 8 * rt;
     if (rg < G) {
 #pragma unroll
@@ -413,43 +474,42 @@ __global__ void __launch_bounds__(kQ4Threads, 3)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           *reinterpret_cast<float4*>(cw + 32 * g + 4 * e) =
-              make_float4(o[4 * g][e] + o[4 * g][2 + e] + zo[g],
-                          o[4 * g + 1][e] + o[4 * g + 1][2 + e] + zo[g],
-                          o[4 * g + 2][e] + o[4 * g + 2][2 + e] + zo[g],
-                          o[4 * g + 3][e] + o[4 * g + 3][2 + e] + zo[g]);
+              make_float4(o[4 * g][e] + o[4 * g][2 + e] + zs[g],
+                          o[4 * g + 1][e] + o[4 * g + 1][2 + e] + zs[g],
+                          o[4 * g + 2][e] + o[4 * g + 2][2 + e] + zs[g],
+                          o[4 * g + 3][e] + o[4 * g + 3][2 + e] + zs[g]);
     }
     __syncthreads();
-    const long long seg0 = start + cur.at;  // the segment's first tile among all
-    const int c0 = (int)(seg0 / per), n = (int)((seg0 + cur.nt - 1) / per) - c0 + 1;
+    const int seg0 = start + cur.at;  // the segment's first tile among all
+    const int c0 = seg0 / per, n = (seg0 + cur.nt - 1) / per - c0 + 1;
     const int me = blockIdx.x - c0;
     const size_t slot = (size_t)2 * G * kQ4Part;  // floats of a CTA's two partials
     float* mine = a.part + (size_t)blockIdx.x * slot + (me == 0 ? slot / 2 : 0);
-#pragma unroll
-    for (int h = 0; h < kQ4MaxG; ++h) {
-      if (h >= G) break;
-      float M = cm[0][h], O = 0.f, L = 0.f;
+    for (int h = warp; h < G; h += kQ4Warps) {
+      float M = cm[0][h], L = 0.f;
 #pragma unroll
       for (int w = 1; w < kQ4Warps; ++w) M = fmaxf(M, cm[w][h]);
+      float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kQ4Warps; ++w) {
         const float f = q4_exp2(cm[w][h] - M);
-        O = fmaf(f, comb[((size_t)w * kQ4MaxG + h) * kKvDim + t], O);
+        const float4 v = reinterpret_cast<const float4*>(comb + ((size_t)w * kQ4MaxG + h) * kKvDim)[lane];
+        O.x = fmaf(f, v.x, O.x);
+        O.y = fmaf(f, v.y, O.y);
+        O.z = fmaf(f, v.z, O.z);
+        O.w = fmaf(f, v.w, O.w);
         L = fmaf(f, cl[w][h], L);
       }
-      if (n == 1) {
-        q4_write(a, cur.b, cur.g, t, h, O / L);
-      } else {
-        mine[h * kQ4Part + t] = O;
-        if (t == 0) mine[h * kQ4Part + kKvDim] = M, mine[h * kQ4Part + kKvDim + 1] = L;
-      }
+      if (n == 1) q4_write(a, cur.b, cur.g, lane, h, O, L);
+      else q4_put(mine + h * kQ4Part, lane, O, M, L);
     }
     if (n > 1) {
       // the last CTA of each 16 merges them into the first one's place, the
       // last of the groups merges the groups
       const int grp = me / kQ4Merge, in = min(kQ4Merge, n - grp * kQ4Merge);
       const int groups = (n + kQ4Merge - 1) / kQ4Merge;
-      const float* base = a.part + (size_t)c0 * slot;  // CTA c0's entry is its second one
-      float* first = const_cast<float*>(base) + (grp ? (size_t)grp * kQ4Merge * slot : slot / 2);
+      float* base = a.part + (size_t)c0 * slot;  // CTA c0's entry is its second one
+      float* first = base + (grp ? (size_t)grp * kQ4Merge * slot : slot / 2);
       __syncthreads();
       if (t == 0) {
         unsigned* tk = a.tick + (grp ? kQ4MaxCtas : 0) + c0 + grp * kQ4Merge;
@@ -458,16 +518,19 @@ __global__ void __launch_bounds__(kQ4Threads, 3)
       }
       __syncthreads();
       if (last) {
-        Q4Merged r;
-        q4_merge(first, base + (size_t)grp * kQ4Merge * slot, slot, in, G, t, r);
-        if (groups > 1) {
-          __syncthreads();
-#pragma unroll
-          for (int h = 0; h < kQ4MaxG; ++h) {
-            if (h >= G) break;
-            first[h * kQ4Part + t] = r.O[h];
-            if (t == 0) first[h * kQ4Part + kKvDim] = r.M[h], first[h * kQ4Part + kKvDim + 1] = r.L[h];
+        // head h is the same warp's from the partials to the result
+        for (int h = warp; h < G; h += kQ4Warps) {
+          float4 O;
+          float M, L;
+          q4_merge(first, base + (size_t)grp * kQ4Merge * slot, slot, in, h, lane, O, M, L);
+          if (groups == 1) {
+            q4_write(a, cur.b, cur.g, lane, h, O, L);
+          } else {
+            __syncwarp();  // every lane has read the first entry
+            q4_put(first + h * kQ4Part, lane, O, M, L);
           }
+        }
+        if (groups > 1) {
           __syncthreads();
           if (t == 0) {
             unsigned* tk = a.tick + 2 * kQ4MaxCtas + c0;
@@ -475,14 +538,13 @@ __global__ void __launch_bounds__(kQ4Threads, 3)
             if (last) *tk = 0;
           }
           __syncthreads();
-          if (last) q4_merge(base + slot / 2, base, kQ4Merge * slot, groups, G, t, r);
-        }
-        if (last) {
-#pragma unroll
-          for (int h = 0; h < kQ4MaxG; ++h) {
-            if (h >= G) break;
-            q4_write(a, cur.b, cur.g, t, h, r.O[h] / r.L[h]);
-          }
+          if (last)
+            for (int h = warp; h < G; h += kQ4Warps) {
+              float4 O;
+              float M, L;
+              q4_merge(base + slot / 2, base, kQ4Merge * slot, groups, h, lane, O, M, L);
+              q4_write(a, cur.b, cur.g, lane, h, O, L);
+            }
         }
       }
     }
@@ -527,7 +589,8 @@ static size_t q4_workspace(int nh, int nkv) {
 
 static bool q4_shape_ok(int B, int nh, int nkv, int d, int S) {
   return B >= 1 && B <= kQ4MaxB && nkv >= 1 && nkv <= 65535 && nh >= 1 && nh % nkv == 0 &&
-         nh / nkv <= kQ4MaxG && d == kKvDim && S >= 1;
+         nh / nkv <= kQ4MaxG && d == kKvDim && S >= 1 &&
+         (long long)B * nkv * (S / kQ4Tile + 1) < (1ll << 30);
 }
 
 }  // namespace ws
@@ -554,7 +617,7 @@ ws_status ws_decode_attention_q4(const float *q, const float *k_new, const float
   }
   if (!q4_shape_ok(B, n_heads, n_kv_heads, head_dim, s_max)) {
     set_error("4-bit decode attention: B 1..%d, head_dim %d, n_heads 1 to %d times n_kv_heads, "
-              "s_max at least 1", kQ4MaxB, kKvDim, kQ4MaxG);
+              "s_max at least 1, fewer than 2^30 tiles of 32 slots", kQ4MaxB, kKvDim, kQ4MaxG);
     return WS_ERR_SHAPE;
   }
   const void* al[] = {q, k_new, v_new, k_cache, v_cache, workspace, out_f32, out_bf16};
