@@ -49,15 +49,21 @@ __device__ __forceinline__ int q4_tiles(int pos, int S) {
   return pos < 0 || pos >= S ? 0 : pos / kQ4Tile + 1;
 }
 
-// Two codes of a word, one in the low nibble of each half, as bf16 (code - 8):
-// 0x4300 | code is 128 + code, and 136 off it is exact.
-__device__ __forceinline__ uint32_t q4_pair(uint32_t m, int i) {
-  const uint32_t v = ((m >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-  const uint32_t c = 0x43084308u;
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&c));
-  return *reinterpret_cast<const uint32_t*>(&r);
+// Two codes, nibble HI of byte 0 and of byte 2 of m, as bf16 f (code - 8) with
+// f = 1/64 (HI 0) or 1/4 (HI 1).  Masked in place, a nibble is the bits of a
+// number on the subnormal grid: code 2^-133 at bits 0..3 and, since the lowest
+// normal binade has the same spacing, code 2^-129 at bits 4..7.  One packed fma
+// by 2^127 brings it to f code and takes 8 f off, all exact; the queries and
+// the results carry 1 / f.
+template <int HI>
+__device__ __forceinline__ uint32_t q4_pair(uint32_t m) {
+  const uint32_t v = m & (HI ? 0x00f000f0u : 0x000f000fu);
+  const uint32_t up = 0x7f007f00u, off = HI ? 0xc000c000u : 0xbe00be00u;  // 2^127; -2, -1/8
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(up), "r"(off));
+  return r;
 }
+constexpr float kQ4Lo = 64.f, kQ4Hi = 4.f;
 
 // v = hi + lo, hi = bf16(v), lo = bf16(v - hi), two values a word
 __device__ __forceinline__ void q4_split(float a, float b, uint32_t& hi, uint32_t& lo) {
@@ -326,6 +332,7 @@ __global__ void __launch_bounds__(kQ4Threads, 3)
         for (int i = 0; i < 8; ++i) {
           v[i] = rg < G ? v[i] * a.scale : 0.f;
           sum += v[i];
+          v[i] *= i & 1 ? kQ4Hi : kQ4Lo;
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
@@ -341,9 +348,9 @@ __global__ void __launch_bounds__(kQ4Threads, 3)
     }
     const uint32_t zmask = rt < 2 ? 0xffffffffu : 0u;
     float o[16][4], m = -1e30f;
-    float2 l = make_float2(0.f, 0.f), zo[4];
-#pragma unroll
-    for (int g = 0; g < 4; ++g) zo[g] = make_float2(0.f, 0.f);
+    // zo: sum p z, column = group (the columns 4 .. 7 repeat them)
+    float zo[4] = {0.f, 0.f, 0.f, 0.f};
+    float2 l = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < 16; ++i)
 #pragma unroll
@@ -380,7 +387,7 @@ __global__ void __launch_bounds__(kQ4Threads, 3)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
               mma_bf16_16816(c, qf[2 * g + k][0], qf[2 * g + k][1], qf[2 * g + k][2],
-                             qf[2 * g + k][3], q4_pair(w, 2 * k), q4_pair(w, 2 * k + 1));
+                             qf[2 * g + k][3], q4_pair<0>(k ? w >> 8 : w), q4_pair<1>(k ? w >> 8 : w));
             s[n] = fma2(make_float2(bf16lo(reinterpret_cast<const uint32_t*>(&ks0)[g]),
                                     bf16lo(reinterpret_cast<const uint32_t*>(&ks1)[g])),
                         add2(make_float2(c[0], c[1]), make_float2(c[2], c[3])), s[n]);
@@ -403,7 +410,7 @@ __global__ void __launch_bounds__(kQ4Threads, 3)
           m = mn;
           l.x *= f, l.y *= f;
 #pragma unroll
-          for (int g = 0; g < 4; ++g) zo[g].x *= f, zo[g].y *= f;
+          for (int e = 0; e < 4; ++e) zo[e] *= f;
 #pragma unroll
           for (int i = 0; i < 16; ++i)
 #pragma unroll
@@ -423,31 +430,38 @@ __global__ void __launch_bounds__(kQ4Threads, 3)
           const unsigned char* sv = st + (kQ4Tile + 16 * u + 2 * rt) * kKvRow;
           uint2 vw[2][2];
           uint4 vs[2][2];
+          uint32_t ph[2], pl[2], bz[2];
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < 2; ++n) {
+            uint32_t z[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const unsigned char* r = sv + (8 * n + e) * kKvRow;
               vw[n][e] = *reinterpret_cast<const uint2*>(r + 8 * rg);
               vs[n][e] = *reinterpret_cast<const uint4*>(r + kKvCodes);
+              z[e] = *reinterpret_cast<const uint32_t*>(r + kKvCodes + 4 * (rg & 3));
             }
+            bz[n] = __byte_perm(z[0], z[1], 0x7632);
+            q4_split(s[2 * u + n].x, s[2 * u + n].y, ph[n], pl[n]);
+          }
+          mma_bf16_16816(zo, ph[0], pl[0], ph[1], pl[1], bz[0], bz[1]);
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            uint32_t ah[2], al[2], mm[2];
+            uint32_t ah[2], al[2], m0[2], m1[2];
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
               const uint32_t z0 = reinterpret_cast<const uint32_t*>(&vs[n][0])[g];
               const uint32_t z1 = reinterpret_cast<const uint32_t*>(&vs[n][1])[g];
               const float2 ps = mul2(s[2 * u + n], make_float2(bf16lo(z0), bf16lo(z1)));
-              zo[g] = fma2(s[2 * u + n], make_float2(bf16hi(z0), bf16hi(z1)), zo[g]);
               q4_split(ps.x, ps.y, ah[n], al[n]);
               const uint32_t w0 = g < 2 ? vw[n][0].x : vw[n][0].y, w1 = g < 2 ? vw[n][1].x : vw[n][1].y;
-              mm[n] = __byte_perm(w0, w1, g & 1 ? 0x7632 : 0x5410);
+              m0[n] = __byte_perm(w0, w1, g & 1 ? 0x0602 : 0x0400);
+              m1[n] = __byte_perm(w0, w1, g & 1 ? 0x0703 : 0x0501);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mma_bf16_16816(o[4 * g + i], ah[0], al[0], ah[1], al[1], q4_pair(mm[0], i),
-                             q4_pair(mm[1], i));
+            mma_bf16_16816(o[4 * g], ah[0], al[0], ah[1], al[1], q4_pair<0>(m0[0]), q4_pair<0>(m0[1]));
+            mma_bf16_16816(o[4 * g + 1], ah[0], al[0], ah[1], al[1], q4_pair<1>(m0[0]), q4_pair<1>(m0[1]));
+            mma_bf16_16816(o[4 * g + 2], ah[0], al[0], ah[1], al[1], q4_pair<0>(m1[0]), q4_pair<0>(m1[1]));
+            mma_bf16_16816(o[4 * g + 3], ah[0], al[0], ah[1], al[1], q4_pair<1>(m1[0]), q4_pair<1>(m1[1]));
           }
         }
       }
@@ -461,11 +475,8 @@ __global__ void __launch_bounds__(kQ4Threads, 3)
     lsum += __shfl_xor_sync(0xffffffffu, lsum, 1);
     lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      zs[g] = zo[g].x + zo[g].y;
-      zs[g] += __shfl_xor_sync(0xffffffffu, zs[g], 1);
-      zs[g] += __shfl_xor_sync(0xffffffffu, zs[g], 2);
-    }
+    for (int g = 0; g < 4; ++g)
+      zs[g] = __shfl_sync(0xffffffffu, zo[g & 1] + zo[2 + (g & 1)], (lane & 28) + (g >> 1));
     if (rt == 0) cm[warp][rg] = m, cl[warp][rg] = lsum;
     float* cw = comb + ((size_t)warp * kQ4MaxG + rg) * kKvDim + 8 * rt;
     if (rg < G) {
@@ -474,10 +485,10 @@ __global__ void __launch_bounds__(kQ4Threads, 3)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           *reinterpret_cast<float4*>(cw + 32 * g + 4 * e) =
-              make_float4(o[4 * g][e] + o[4 * g][2 + e] + zs[g],
-                          o[4 * g + 1][e] + o[4 * g + 1][2 + e] + zs[g],
-                          o[4 * g + 2][e] + o[4 * g + 2][2 + e] + zs[g],
-                          o[4 * g + 3][e] + o[4 * g + 3][2 + e] + zs[g]);
+              make_float4(fmaf(o[4 * g + 0][e] + o[4 * g + 0][2 + e], kQ4Lo, zs[g]),
+                          fmaf(o[4 * g + 1][e] + o[4 * g + 1][2 + e], kQ4Hi, zs[g]),
+                          fmaf(o[4 * g + 2][e] + o[4 * g + 2][2 + e], kQ4Lo, zs[g]),
+                          fmaf(o[4 * g + 3][e] + o[4 * g + 3][2 + e], kQ4Hi, zs[g]));
     }
     __syncthreads();
     const int seg0 = start + cur.at;  // the segment's first tile among all
