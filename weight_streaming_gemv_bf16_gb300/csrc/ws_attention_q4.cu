@@ -65,6 +65,15 @@ __device__ __forceinline__ uint32_t q4_pair(uint32_t m) {
 }
 constexpr float kQ4Lo = 64.f, kQ4Hi = 4.f;
 
+// d = A B: the product whose sum starts here, with no registers to clear first
+__device__ __forceinline__ void q4_mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // v = hi + lo, hi = bf16(v), lo = bf16(v - hi), two values a word
 __device__ __forceinline__ void q4_split(float a, float b, uint32_t& hi, uint32_t& lo) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -215,11 +224,13 @@ __device__ __forceinline__ void q4_put(float* e, int lane, float4 O, float M, fl
   if (lane == 0) *reinterpret_cast<float2*>(e + kKvDim) = make_float2(M, L);
 }
 
-__global__ void __launch_bounds__(kQ4Threads, 3)
+__global__ void __launch_bounds__(kQ4Threads, 2)
     k_decode_attention_q4(const __grid_constant__ AttnQ4Params a) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t full[kQ4Warps][kQ4Stages];
   __shared__ float cm[kQ4Warps][kQ4MaxG], cl[kQ4Warps][kQ4MaxG];
+  __shared__ uint4 qfrag[8][32];
+  __shared__ float qsum[kQ4MaxG][4];
   __shared__ int last;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, G = a.G;
   const int rg = lane >> 2, rt = lane & 3;  // row and column of the fragments
@@ -315,36 +326,38 @@ __global__ void __launch_bounds__(kQ4Threads, 3)
   while (x0 < run) {  // one (row, head) at a time
     q4_seek(a, cur, x0);
     const int x1 = min(run, cur.at + cur.nt);
-    // the queries as the first product's A operand: head rg in rows rg (hi
-    // terms) and rg + 8 (lo terms); lane rt of a quad holds dimensions
-    // 32 g + 8 rt .. + 7, in the order of the key row's nibbles.  qz: their
-    // sums per group, the operand against the zeros (k = group)
-    uint32_t qf[8][4], qz[2];
+    // the queries as the first product's A operand, in shared memory (held in
+    // registers they cost a CTA a SM its place): head rg in rows rg (hi terms)
+    // and rg + 8 (lo terms); lane rt of a quad holds dimensions 32 g + 8 rt ..
+    // + 7, in the order of the key row's nibbles; warp g makes group g's.  qz:
+    // their sums per group, the operand against the zeros (k = group)
     {
+      static_assert(kQ4Warps == 4, "a warp per group");
       const float* qr = a.q + ((size_t)cur.b * a.nh + (size_t)cur.g * G + (rg < G ? rg : 0)) * kKvDim;
-      float sums[4];
+      float v[8], sum = 0.f;
+      load8<DT_F32>(qr + 32 * warp + 8 * rt, v);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        float v[8];
-        load8<DT_F32>(qr + 32 * g + 8 * rt, v);
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[i] = rg < G ? v[i] * a.scale : 0.f;
-          sum += v[i];
-          v[i] *= i & 1 ? kQ4Hi : kQ4Lo;
-        }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        sums[g] = sum;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          q4_split(v[2 * s], v[2 * s + 4], qf[2 * g + s][0], qf[2 * g + s][1]);
-          q4_split(v[2 * s + 1], v[2 * s + 5], qf[2 * g + s][2], qf[2 * g + s][3]);
-        }
+      for (int i = 0; i < 8; ++i) {
+        v[i] = rg < G ? v[i] * a.scale : 0.f;
+        sum += v[i];
+        v[i] *= i & 1 ? kQ4Hi : kQ4Lo;
       }
-      q4_split(rt == 0 ? sums[0] : rt == 1 ? sums[2] : 0.f, rt == 0 ? sums[1] : rt == 1 ? sums[3] : 0.f,
-               qz[0], qz[1]);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      if (rt == 0) qsum[rg][warp] = sum;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint4 f;
+        q4_split(v[2 * k], v[2 * k + 4], f.x, f.y);
+        q4_split(v[2 * k + 1], v[2 * k + 5], f.z, f.w);
+        qfrag[2 * warp + k][lane] = f;
+      }
+    }
+    __syncthreads();
+    uint32_t qz[2];
+    {
+      const float2 z = rt < 2 ? *reinterpret_cast<const float2*>(&qsum[rg][2 * rt]) : make_float2(0.f, 0.f);
+      q4_split(z.x, z.y, qz[0], qz[1]);
     }
     const uint32_t zmask = rt < 2 ? 0xffffffffu : 0u;
     float o[16][4], m = -1e30f;
@@ -370,27 +383,34 @@ __global__ void __launch_bounds__(kQ4Threads, 3)
         // scores: head rg, slots 8 n + 2 rt + e
         float2 s[4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const unsigned char* kr = st + (8 * n + rg) * kKvRow;
-          const uint4 kw = *reinterpret_cast<const uint4*>(kr + 16 * rt);
-          const uint2 kz = *reinterpret_cast<const uint2*>(kr + kKvCodes + 8 * (rt & 1));
-          const unsigned char* ksp = st + (8 * n + 2 * rt) * kKvRow + kKvCodes;
-          const uint4 ks0 = *reinterpret_cast<const uint4*>(ksp);
-          const uint4 ks1 = *reinterpret_cast<const uint4*>(ksp + kKvRow);
-          float cz[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_bf16_16816(cz, qz[0], qz[1], 0u, 0u, __byte_perm(kz.x, kz.y, 0x7632) & zmask, 0u);
-          s[n] = add2(make_float2(cz[0], cz[1]), make_float2(cz[2], cz[3]));
+        for (int u = 0; u < 2; ++u) {
+          uint4 kw[2], ks[2][2];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const unsigned char* kr = st + (16 * u + 8 * n + rg) * kKvRow;
+            kw[n] = *reinterpret_cast<const uint4*>(kr + 16 * rt);
+            const uint2 kz = *reinterpret_cast<const uint2*>(kr + kKvCodes + 8 * (rt & 1));
+            const unsigned char* ksp = st + (16 * u + 8 * n + 2 * rt) * kKvRow + kKvCodes;
+            ks[n][0] = *reinterpret_cast<const uint4*>(ksp);
+            ks[n][1] = *reinterpret_cast<const uint4*>(ksp + kKvRow);
+            float cz[4];
+            q4_mma0(cz, qz[0], qz[1], 0u, 0u, __byte_perm(kz.x, kz.y, 0x7632) & zmask, 0u);
+            s[2 * u + n] = add2(make_float2(cz[0], cz[1]), make_float2(cz[2], cz[3]));
+          }
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const uint32_t w = reinterpret_cast<const uint32_t*>(&kw)[g];
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint4 q0 = qfrag[2 * g][lane], q1 = qfrag[2 * g + 1][lane];
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              mma_bf16_16816(c, qf[2 * g + k][0], qf[2 * g + k][1], qf[2 * g + k][2],
-                             qf[2 * g + k][3], q4_pair<0>(k ? w >> 8 : w), q4_pair<1>(k ? w >> 8 : w));
-            s[n] = fma2(make_float2(bf16lo(reinterpret_cast<const uint32_t*>(&ks0)[g]),
-                                    bf16lo(reinterpret_cast<const uint32_t*>(&ks1)[g])),
-                        add2(make_float2(c[0], c[1]), make_float2(c[2], c[3])), s[n]);
+            for (int n = 0; n < 2; ++n) {
+              const uint32_t w = reinterpret_cast<const uint32_t*>(&kw[n])[g], w8 = w >> 8;
+              float c[4];
+              q4_mma0(c, q0.x, q0.y, q0.z, q0.w, q4_pair<0>(w), q4_pair<1>(w));
+              mma_bf16_16816(c, q1.x, q1.y, q1.z, q1.w, q4_pair<0>(w8), q4_pair<1>(w8));
+              s[2 * u + n] = fma2(make_float2(bf16lo(reinterpret_cast<const uint32_t*>(&ks[n][0])[g]),
+                                              bf16lo(reinterpret_cast<const uint32_t*>(&ks[n][1])[g])),
+                                  add2(make_float2(c[0], c[1]), make_float2(c[2], c[3])),
+                                  s[2 * u + n]);
+            }
           }
         }
         if ((x - cur.at + 1) * kQ4Tile > cur.pos + 1) {
