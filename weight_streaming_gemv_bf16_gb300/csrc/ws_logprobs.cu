@@ -11,7 +11,16 @@
 
 namespace ws {
 
-constexpr int kMaxTop = 32;
+constexpr int kMaxTop = 32;         // alternatives a row: one a lane
+constexpr int kLpThreads = 256;
+constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kLpEach = 16;         // values a thread takes at once
+constexpr int kLpStep = kLpThreads * kLpEach;
+constexpr int kLpCompact = 512;     // candidates that make the CTA sort out the best ones
+constexpr int kLpBuf = kLpCompact + kLpStep + 2 * kLpEach;
+constexpr int kLpCtas = 608;        // CTAs that a small batch's rows are cut into
+constexpr float kLpFar = -1e4f;     // e^y is 0 long before: stands for -infinity in sums
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct LogprobParams {
   const void* x;  // [rows][ld], the first V of each row
@@ -22,16 +31,12 @@ struct LogprobParams {
   float* top_lp;
   long long ld;
   int V, k;
+  int splits, chunk;           // CTAs a row, values a CTA
+  unsigned* tick;              // [rows]
+  float4* stat;                // [rows][splits]: max, sum, sum e y
+  unsigned long long* keys;    // [rows][splits][k]
   int* err;
 };
-
-template <int DT>
-__device__ __forceinline__ float logit(const void* row, int i) {
-  if constexpr (DT == DT_F32) return static_cast<const float*>(row)[i];
-  const uint16_t u = static_cast<const uint16_t*>(row)[i];
-  if constexpr (DT == DT_F16) return __half2float(__ushort_as_half(u));
-  return __uint_as_float((uint32_t)u << 16);
-}
 
 // A key that orders as (value, lower index): the value's bits made monotone,
 // then the complement of the index.  0 below every key; NaN has none.
@@ -49,63 +54,367 @@ __device__ __forceinline__ float key_value(unsigned long long k) {
   return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
 }
 
-template <typename T, typename F>
-__device__ __forceinline__ T cta_reduce(T v, F f, T* red) {
-  const int t = threadIdx.x;
-  red[t] = v;
-  __syncthreads();
-  for (int o = blockDim.x >> 1; o > 0; o >>= 1) {
-    if (t < o) red[t] = f(red[t], red[t + o]);
-    __syncthreads();
-  }
-  const T r = red[0];
-  __syncthreads();
+__device__ __forceinline__ float lp_exp(float y) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y * kLog2e));
   return r;
 }
 
-// One CTA per row: the maximum, the sums, then one pass per alternative.
+// Largest, sum of e^(x - max) and sum of e^(x - max) (x - max) of some values.
+// m starts at the lowest number, so that x - m is defined for every x but
+// +infinity and NaN, which make the sums NaN.
+struct LpSum {
+  float m, z, t;
+  __device__ __forceinline__ void raise(float to) {  // m to `to` >= m
+    const float d = fmaxf(m - to, kLpFar), f = lp_exp(d);
+    t = z > 0.f ? f * fmaf(z, d, t) : t;
+    z *= f;
+    m = to;
+  }
+  __device__ __forceinline__ void add_diff(float d) {  // one value, x - m given
+    const float y = max_nan(d, kLpFar), e = lp_exp(y);
+    z += e;
+    t = fmaf(e, y, t);
+  }
+  __device__ __forceinline__ void join(const LpSum& o) {
+    if (o.m > m) raise(o.m);
+    const float d = fmaxf(o.m - m, kLpFar), f = o.m == m ? 1.f : lp_exp(d);
+    const bool inf = m == INFINITY;  // both sides' sums are NaN then, where they met it
+    z = fmaf(o.z, f, z);
+    if (o.z != 0.f) t = fmaf(f, inf ? o.t : fmaf(o.z, d, o.t), t);
+  }
+};
+
+// 16 values in registers as they came; the largest; x - m of each; each value
 template <int DT>
-__global__ void __launch_bounds__(256) k_token_logprobs(const __grid_constant__ LogprobParams a) {
-  __shared__ float red[256];
-  __shared__ unsigned long long kred[256];
-  const int r = blockIdx.x, t = threadIdx.x, V = a.V;
-  const char* row = static_cast<const char*>(a.x) + (size_t)r * a.ld * (DT == DT_F32 ? 4 : 2);
-  float m = -INFINITY;
-  for (int i = t; i < V; i += 256) m = max_nan(m, logit<DT>(row, i));
-  m = cta_reduce(m, [](float x, float y) { return max_nan(x, y); }, red);
-  float z = 0.f, e = 0.f;
-  for (int i = t; i < V; i += 256) {
-    const float y = logit<DT>(row, i) - m, p = expf(y);
-    z += p;
-    if (p != 0.f) e = fmaf(p, y, e);
+struct LpRegs {
+  static constexpr int kVec = DT == DT_F32 ? 4 : 8;  // values a 16-byte load
+  uint4 u[kLpEach / kVec];
+  __device__ __forceinline__ float value(int i) const {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
+    if constexpr (DT == DT_F32) return __uint_as_float(w[i]);
+    const uint32_t h = w[i >> 1];
+    if constexpr (DT == DT_F16) {
+      const __half2 v = *reinterpret_cast<const __half2*>(&h);
+      return i & 1 ? __high2float(v) : __low2float(v);
+    }
+    return i & 1 ? bf16hi(h) : bf16lo(h);
   }
-  z = cta_reduce(z, [](float x, float y) { return x + y; }, red);
-  e = cta_reduce(e, [](float x, float y) { return x + y; }, red);
-  const float lz = logf(z);
-  if (t == 0) {
-    if (a.entropy) a.entropy[r] = lz - e / z;
-    if (a.targets && a.logprob) {
-      const int i = a.targets[r];
-      if (i >= V) atomicExch(a.err, kDerrBadToken);
-      a.logprob[r] = i < 0 ? 0.f : i >= V ? NAN : logit<DT>(row, i) - m - lz;
+  __device__ __forceinline__ float largest() const {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
+    if constexpr (DT == DT_F32) {
+      float m = value(0);
+#pragma unroll
+      for (int i = 1; i < kLpEach; ++i) m = fmaxf(m, value(i));
+      return m;
+    } else if constexpr (DT == DT_BF16) {
+      __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&w[0]);
+#pragma unroll
+      for (int i = 1; i < kLpEach / 2; ++i)
+        m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+      return fmaxf(__low2float(m), __high2float(m));
+    } else {
+      __half2 m = *reinterpret_cast<const __half2*>(&w[0]);
+#pragma unroll
+      for (int i = 1; i < kLpEach / 2; ++i) m = __hmax2(m, *reinterpret_cast<const __half2*>(&w[i]));
+      return fmaxf(__low2float(m), __high2float(m));
     }
   }
-  unsigned long long last = ~0ull;
-  for (int j = 0; j < a.k; ++j) {
-    unsigned long long best = 0;
-    for (int i = t; i < V; i += 256) {
-      const unsigned long long key = top_key(logit<DT>(row, i), i);
-      if (key < last && key > best) best = key;
+  // x - m, one rounding: for the 16-bit types by the mixed fma 1 x + (-m)
+  __device__ __forceinline__ float diff(int i, float neg_m) const {
+    if constexpr (DT == DT_F32) {
+      return value(i) + neg_m;
+    } else {
+      const uint32_t h = reinterpret_cast<const uint32_t*>(u)[i >> 1];
+      float r;
+      if constexpr (DT == DT_BF16) {
+        if (i & 1)
+          asm("{\n\t.reg .b16 l, h, o;\n\tmov.b32 {l, h}, %1;\n\tmov.b16 o, 0x3f80;\n\t"
+              "fma.rn.f32.bf16 %0, h, o, %2;\n\t}" : "=f"(r) : "r"(h), "f"(neg_m));
+        else
+          asm("{\n\t.reg .b16 l, h, o;\n\tmov.b32 {l, h}, %1;\n\tmov.b16 o, 0x3f80;\n\t"
+              "fma.rn.f32.bf16 %0, l, o, %2;\n\t}" : "=f"(r) : "r"(h), "f"(neg_m));
+      } else {
+        if (i & 1)
+          asm("{\n\t.reg .b16 l, h, o;\n\tmov.b32 {l, h}, %1;\n\tmov.b16 o, 0x3c00;\n\t"
+              "fma.rn.f32.f16 %0, h, o, %2;\n\t}" : "=f"(r) : "r"(h), "f"(neg_m));
+        else
+          asm("{\n\t.reg .b16 l, h, o;\n\tmov.b32 {l, h}, %1;\n\tmov.b16 o, 0x3c00;\n\t"
+              "fma.rn.f32.f16 %0, l, o, %2;\n\t}" : "=f"(r) : "r"(h), "f"(neg_m));
+      }
+      return r;
     }
-    best = cta_reduce(best, [](unsigned long long x, unsigned long long y) { return x > y ? x : y; },
-                      kred);
-    last = best;
+  }
+};
+
+// The lanes' keys in falling order; then merged with a list in falling order.
+__device__ __forceinline__ unsigned long long lp_exchange(unsigned long long k, int o, bool keep_max) {
+  const unsigned long long p = __shfl_xor_sync(0xffffffffu, k, o);
+  return (p > k) == keep_max ? p : k;
+}
+__device__ __forceinline__ unsigned long long lp_sort(unsigned long long k, int lane) {
+#pragma unroll
+  for (int n = 2; n <= 32; n <<= 1)
+#pragma unroll
+    for (int o = n >> 1; o > 0; o >>= 1)
+      k = lp_exchange(k, o, ((lane & o) == 0) == ((lane & n) == 0 || n == 32));
+  return k;
+}
+__device__ __forceinline__ unsigned long long lp_merge(unsigned long long a, unsigned long long b,
+                                                       int lane) {
+  const unsigned long long r = __shfl_sync(0xffffffffu, b, 31 - lane);
+  a = a > r ? a : r;  // the 32 largest of both, rising then falling
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a = lp_exchange(a, o, (lane & o) == 0);
+  return a;
+}
+
+struct LpShared {
+  unsigned long long buf[kLpBuf];
+  unsigned long long list[kLpWarps][32];
+  unsigned long long thr;   // a candidate's key is at least this
+  int n;                    // candidates
+  LpSum sums[kLpWarps];
+  int last;
+};
+
+// The whole CTA: the 32 largest of the candidates, in falling order, become
+// the only ones.  bar: the threshold becomes the k-th of them, plus `plus`.
+__device__ __forceinline__ void lp_compact(LpShared& sh, int n, int k, int plus) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  unsigned long long mine = 0;
+  for (int i = warp * 32; i < n; i += kLpThreads) {
+    const unsigned long long key = i + lane < n ? sh.buf[i + lane] : 0;
+    if (__any_sync(0xffffffffu, key > __shfl_sync(0xffffffffu, mine, k - 1)))
+      mine = lp_merge(mine, lp_sort(key, lane), lane);
+  }
+  sh.list[warp][lane] = mine;
+  __syncthreads();
+  if (warp == 0) {
+    for (int w = 1; w < kLpWarps; ++w) {
+      if (w * 32 >= n) break;
+      mine = lp_merge(mine, sh.list[w][lane], lane);
+    }
+    sh.buf[lane] = mine;
+    if (lane == k - 1) sh.thr = mine ? mine + plus : 0;
+    const int have = __popc(__ballot_sync(0xffffffffu, mine != 0));
+    if (lane == 0) sh.n = have;
+  }
+  __syncthreads();
+}
+
+// One CTA per (split, row).  DRAM bound: 64 bytes (32 of the 16-bit types) a
+// thread are in flight while the last ones are worked on, one barrier for
+// every 4096 values.  The best `k` are found in the same pass: the k-th of the
+// threads' best values of the first step bounds the k-th of all from below, so
+// that only the few values from there on become candidates; their best ones
+// raise the bound when there are many, which an order that keeps rising makes
+// slower but not wrong.
+template <int DT, bool TOP>
+__global__ void __launch_bounds__(kLpThreads) k_token_logprobs(const __grid_constant__ LogprobParams a) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  LpShared& sh = *reinterpret_cast<LpShared*>(smem);
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int r = blockIdx.x / a.splits, sp = blockIdx.x - r * a.splits;
+  constexpr int kSize = DT == DT_F32 ? 4 : 2, kVec = LpRegs<DT>::kVec;
+  const char* row = static_cast<const char*>(a.x) + (size_t)r * a.ld * kSize;
+  const int c0 = sp * a.chunk, c1 = min(a.V, c0 + a.chunk);
+  // values before the first 16-byte boundary and behind the last: one a thread
+  const int pre = min(c1 - c0, (int)((16 - ((uintptr_t)(row + (size_t)c0 * kSize) & 15)) & 15) / kSize);
+  const int v0 = c0 + pre, nv = (c1 - v0) / kVec, rest = (c1 - v0) - nv * kVec;
+  const uint4* body = reinterpret_cast<const uint4*>(row + (size_t)v0 * kSize);
+
+  LpRegs<DT> cur, nxt;
+  constexpr int kLoads = kLpEach / kVec;
+  constexpr uint32_t kNegInf = DT == DT_F32 ? 0xff800000u : DT == DT_BF16 ? 0xff80ff80u : 0xfc00fc00u;
+  auto load = [&](LpRegs<DT>& g, int at) {  // vectors at + j * 256 + t; -infinity behind the end
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int i = at + j * kLpThreads + t;
+      g.u[j] = i < nv ? __ldcs(body + i) : make_uint4(kNegInf, kNegInf, kNegInf, kNegInf);
+    }
+  };
+  constexpr int kStepVec = kLpThreads * kLoads;
+  load(cur, 0);
+
+  LpSum s = {-FLT_MAX, 0.f, 0.f};
+  unsigned long long thr = 0;
+  float thrv = -INFINITY;
+  if (TOP) {
+    if (t == 0) sh.n = 0;
+    __syncthreads();
+  }
+  int over = 0;
+  auto candidate = [&](float v, int i) {
+    const unsigned long long key = top_key(v, i);
+    if (key >= thr && key) {
+      const int at = atomicAdd(&sh.n, 1);
+      sh.buf[at] = key;
+      over = at;
+    }
+  };
+  if (t < pre + rest) {
+    const int i = t < pre ? c0 + t : v0 + nv * kVec + (t - pre);
+    float x;
+    if constexpr (DT == DT_F32) x = reinterpret_cast<const float*>(row)[i];
+    else if constexpr (DT == DT_F16) x = __half2float(reinterpret_cast<const __half*>(row)[i]);
+    else x = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[i] << 16);
+    if (x > s.m) s.m = x;
+    s.add_diff(x - s.m);
+    if (TOP) candidate(x, i);
+  }
+  for (int at = 0; at < nv; at += kStepVec) {
+    if (at + kStepVec < nv) load(nxt, at + kStepVec);
+    const float mx = cur.largest();
+    if (mx > s.m) s.raise(mx);
+    const float nm = -s.m;
+#pragma unroll
+    for (int i = 0; i < kLpEach; ++i) s.add_diff(cur.diff(i, nm));
+    if (TOP) {
+      if (at == 0) {
+        // the threads' best values, over what the candidates will hold
+        unsigned long long best = 0;
+#pragma unroll
+        for (int i = 0; i < kLpEach; ++i) {
+          const int e = v0 + ((i / kVec) * kLpThreads + t) * kVec + i % kVec;
+          const float v = cur.value(i);
+          const unsigned long long key = v == mx && (i / kVec) * kLpThreads + t < nv ? top_key(v, e) : 0;
+          best = key > best ? key : best;
+        }
+        const int have = sh.n;  // the odd values at the ends, kept behind
+        unsigned long long odd = 0;
+        __syncthreads();
+        if (t < have) odd = sh.buf[t];
+        __syncthreads();
+        sh.buf[t] = best;
+        __syncthreads();
+        lp_compact(sh, kLpThreads, a.k, 0);
+        thr = sh.thr;
+        thrv = thr ? key_value(thr) : -INFINITY;
+        __syncthreads();
+        if (t < have) sh.buf[t] = odd;
+        if (t == 0) sh.n = have;
+        __syncthreads();
+      }
+      if (mx >= thrv) {
+#pragma unroll
+        for (int i = 0; i < kLpEach; ++i) {
+          const float v = cur.value(i);
+          const int vec = at + (i / kVec) * kLpThreads + t;
+          if (v >= thrv && vec < nv) candidate(v, v0 + vec * kVec + i % kVec);
+        }
+      }
+      if (__syncthreads_or(over >= kLpCompact)) {
+        lp_compact(sh, sh.n, a.k, 1);
+        thr = sh.thr;
+        thrv = thr ? key_value(thr) : -INFINITY;
+        over = 0;
+        __syncthreads();
+      }
+    }
+    cur = nxt;
+  }
+  if (TOP) {
+    __syncthreads();
+    lp_compact(sh, sh.n, a.k, 1);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    LpSum p;
+    p.m = __shfl_xor_sync(0xffffffffu, s.m, o);
+    p.z = __shfl_xor_sync(0xffffffffu, s.z, o);
+    p.t = __shfl_xor_sync(0xffffffffu, s.t, o);
+    // the same order on both sides, so that the lanes agree to the bit
+    if (lane & o) {
+      p.join(s);
+      s = p;
+    } else {
+      s.join(p);
+    }
+  }
+  if (lane == 0) sh.sums[warp] = s;
+  __syncthreads();
+  if (a.splits > 1) {
+    const size_t at = (size_t)r * a.splits;
     if (t == 0) {
-      if (a.top_idx) a.top_idx[(size_t)r * a.k + j] = best ? key_index(best) : -1;
-      if (a.top_lp) a.top_lp[(size_t)r * a.k + j] = best ? key_value(best) - m - lz : NAN;
+      for (int w = 1; w < kLpWarps; ++w) s.join(sh.sums[w]);
+      a.stat[at + sp] = make_float4(s.m, s.z, s.t, 0.f);
     }
+    if (TOP && t < a.k) a.keys[(at + sp) * a.k + t] = sh.buf[t];
+    __syncthreads();
+    if (t == 0) {
+      unsigned old;
+      asm volatile("atom.add.acq_rel.gpu.u32 %0, [%1], 1;" : "=r"(old) : "l"(a.tick + r) : "memory");
+      sh.last = old == (unsigned)(a.splits - 1);
+      if (sh.last) a.tick[r] = 0;
+    }
+    __syncthreads();
+    if (!sh.last) return;
+    // the row's last CTA: the splits' sums in their order, and the best of
+    // their best
+    if (TOP) {
+      const int n = a.splits * a.k;
+      for (int i = t; i < n; i += kLpThreads) sh.buf[i] = __ldcg(a.keys + at * a.k + i);
+      __syncthreads();
+      lp_compact(sh, n, a.k, 1);
+    }
+    if (t == 0) {
+      float4 v = __ldcg(a.stat + at);
+      s = {v.x, v.y, v.z};
+      for (int i = 1; i < a.splits; ++i) {
+        v = __ldcg(a.stat + at + i);
+        s.join({v.x, v.y, v.z});
+      }
+    }
+  } else if (t == 0) {
+    for (int w = 1; w < kLpWarps; ++w) s.join(sh.sums[w]);
+  }
+  if (t == 0) sh.sums[0] = s;
+  __syncthreads();
+  s = sh.sums[0];
+  const float lz = logf(s.z);
+  if (t == 0) {
+    if (a.entropy) a.entropy[r] = lz - s.t / s.z;
+    if (a.targets) {
+      const int i = a.targets[r];
+      float lp = 0.f;
+      if (i >= a.V) {
+        atomicExch(a.err, kDerrBadToken);
+        lp = NAN;
+      } else if (i >= 0) {
+        float x;
+        if constexpr (DT == DT_F32) x = reinterpret_cast<const float*>(row)[i];
+        else if constexpr (DT == DT_F16) x = __half2float(reinterpret_cast<const __half*>(row)[i]);
+        else x = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[i] << 16);
+        lp = x - s.m - lz;
+      }
+      a.logprob[r] = lp;
+    }
+  }
+  if (TOP && t < a.k) {
+    const unsigned long long key = sh.buf[t];
+    if (a.top_idx) a.top_idx[(size_t)r * a.k + t] = key ? key_index(key) : -1;
+    if (a.top_lp) a.top_lp[(size_t)r * a.k + t] = key ? key_value(key) - s.m - lz : NAN;
   }
 }
+
+// Splits of a row, and values a split: whole steps, and no more than fill
+// kLpCtas CTAs with all rows (a row alone on one CTA takes 40 times as long).
+static void lp_split(int rows, int V, int& splits, int& chunk) {
+  const int steps = (V + kLpStep - 1) / kLpStep;
+  int want = kLpCtas / rows;
+  if (want > 64) want = 64;
+  if (want < 1) want = 1;
+  const int per = (steps + want - 1) / want;
+  chunk = per * kLpStep;
+  splits = (steps + per - 1) / per;
+}
+
+// rows on several CTAs are at most kLpCtas / 2; the tickets' place is the same
+// for every shape, so that no call finds another's results there
+constexpr size_t kLpTick = (kLpCtas / 2 * 4 + 255) / 256 * 256;
+
+static size_t lp_align(size_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace ws
 
@@ -115,7 +424,10 @@ extern "C" {
 
 size_t ws_logprobs_workspace_bytes(int rows, int V, int topk) {
   if (rows < 1 || V < 1 || topk < 0 || topk > kMaxTop || topk > V) return 0;
-  return 256;
+  int splits, chunk;
+  lp_split(rows, V, splits, chunk);
+  if (splits == 1) return 256;
+  return kLpTick + lp_align((size_t)rows * splits * 16) + (size_t)rows * splits * topk * 8;
 }
 
 ws_status ws_token_logprobs(const void *logits, int dtype, long long ld, const int32_t *targets,
@@ -160,10 +472,25 @@ ws_status ws_token_logprobs(const void *logits, int dtype, long long ld, const i
     set_error("device error flag unavailable");
     return WS_ERR_CUDA;
   }
+  lp_split(rows, V, a.splits, a.chunk);
+  char* w = static_cast<char*>(workspace);
+  a.tick = reinterpret_cast<unsigned*>(w);
+  w += kLpTick;
+  a.stat = reinterpret_cast<float4*>(w);
+  a.keys = reinterpret_cast<unsigned long long*>(w + lp_align((size_t)rows * a.splits * 16));
   cudaStream_t st = (cudaStream_t)stream;
-  if (dtype == WS_DTYPE_F32) k_token_logprobs<DT_F32><<<rows, 256, 0, st>>>(a);
-  else if (dtype == WS_DTYPE_BF16) k_token_logprobs<DT_BF16><<<rows, 256, 0, st>>>(a);
-  else k_token_logprobs<DT_F16><<<rows, 256, 0, st>>>(a);
+  const int grid = rows * a.splits;
+  const int sm = sizeof(LpShared);
+  if (dtype == WS_DTYPE_F32) {
+    if (topk) k_token_logprobs<DT_F32, true><<<grid, kLpThreads, sm, st>>>(a);
+    else k_token_logprobs<DT_F32, false><<<grid, kLpThreads, sm, st>>>(a);
+  } else if (dtype == WS_DTYPE_BF16) {
+    if (topk) k_token_logprobs<DT_BF16, true><<<grid, kLpThreads, sm, st>>>(a);
+    else k_token_logprobs<DT_BF16, false><<<grid, kLpThreads, sm, st>>>(a);
+  } else {
+    if (topk) k_token_logprobs<DT_F16, true><<<grid, kLpThreads, sm, st>>>(a);
+    else k_token_logprobs<DT_F16, false><<<grid, kLpThreads, sm, st>>>(a);
+  }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("launch failed: %s", cudaGetErrorString(e));
