@@ -16,8 +16,10 @@ constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpEach = 16;         // values a thread takes at once
 constexpr int kLpStep = kLpThreads * kLpEach;
-constexpr int kLpCompact = 512;     // candidates that make the CTA sort out the best ones
+constexpr int kLpCompact = 64;      // candidates that make the CTA sort out the best ones
 constexpr int kLpBuf = kLpCompact + kLpStep + 2 * kLpEach;
+static_assert(kLpBuf >= 64 * kMaxTop, "the splits' best fit");
+constexpr int kLpSplits = 64;       // CTAs a row at most
 constexpr int kLpCtas = 608;        // CTAs that a small batch's rows are cut into
 constexpr float kLpFar = -1e4f;     // e^y is 0 long before: stands for -infinity in sums
 constexpr float kLog2e = 1.4426950408889634f;
@@ -54,34 +56,51 @@ __device__ __forceinline__ float key_value(unsigned long long k) {
   return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
 }
 
-__device__ __forceinline__ float lp_exp(float y) {
+__device__ __forceinline__ float lp_exp2(float y) {
   float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y * kLog2e));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
   return r;
 }
 
-// Largest, sum of e^(x - max) and sum of e^(x - max) (x - max) of some values.
-// m starts at the lowest number, so that x - m is defined for every x but
-// +infinity and NaN, which make the sums NaN.
+// Largest, sum of e^(x - max) and sum of e^(x - max) log2 e (x - max) of some
+// values.  m starts at the lowest number, so that x - m is defined for every x
+// but +infinity and NaN, which make the sums NaN.
 struct LpSum {
   float m, z, t;
   __device__ __forceinline__ void raise(float to) {  // m to `to` >= m
-    const float d = fmaxf(m - to, kLpFar), f = lp_exp(d);
+    const float d = fmaxf(m - to, kLpFar) * kLog2e, f = lp_exp2(d);
     t = z > 0.f ? f * fmaf(z, d, t) : t;
     z *= f;
     m = to;
   }
   __device__ __forceinline__ void add_diff(float d) {  // one value, x - m given
-    const float y = max_nan(d, kLpFar), e = lp_exp(y);
+    const float y = max_nan(d, kLpFar) * kLog2e, e = lp_exp2(y);
     z += e;
     t = fmaf(e, y, t);
   }
   __device__ __forceinline__ void join(const LpSum& o) {
     if (o.m > m) raise(o.m);
-    const float d = fmaxf(o.m - m, kLpFar), f = o.m == m ? 1.f : lp_exp(d);
-    const bool inf = m == INFINITY;  // both sides' sums are NaN then, where they met it
+    const float d = o.m == m ? 0.f : fmaxf(o.m - m, kLpFar) * kLog2e, f = lp_exp2(d);
     z = fmaf(o.z, f, z);
-    if (o.z != 0.f) t = fmaf(f, inf ? o.t : fmaf(o.z, d, o.t), t);
+    if (o.z != 0.f) t = fmaf(f, fmaf(o.z, d, o.t), t);
+  }
+  // over `n` lanes (a power of two); the lanes agree to the bit
+  __device__ __forceinline__ void join_lanes(int n) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      if (o >= n) break;
+      LpSum p;
+      p.m = __shfl_xor_sync(0xffffffffu, m, o);
+      p.z = __shfl_xor_sync(0xffffffffu, z, o);
+      p.t = __shfl_xor_sync(0xffffffffu, t, o);
+      if (lane & o) {
+        p.join(*this);
+        *this = p;
+      } else {
+        join(p);
+      }
+    }
   }
 };
 
@@ -188,13 +207,16 @@ __device__ __forceinline__ void lp_compact(LpShared& sh, int n, int k, int plus)
     if (__any_sync(0xffffffffu, key > __shfl_sync(0xffffffffu, mine, k - 1)))
       mine = lp_merge(mine, lp_sort(key, lane), lane);
   }
-  sh.list[warp][lane] = mine;
+  // the warps' lists in pairs; those past the candidates are empty
+  const int lists = min(kLpWarps, (n + 31) / 32);
+#pragma unroll 1
+  for (int o = 1; o < lists; o <<= 1) {
+    if ((warp & (2 * o - 1)) == o) sh.list[warp][lane] = mine;
+    __syncthreads();
+    if (!(warp & (2 * o - 1)) && warp + o < lists) mine = lp_merge(mine, sh.list[warp + o][lane], lane);
+  }
   __syncthreads();
   if (warp == 0) {
-    for (int w = 1; w < kLpWarps; ++w) {
-      if (w * 32 >= n) break;
-      mine = lp_merge(mine, sh.list[w][lane], lane);
-    }
     sh.buf[lane] = mine;
     if (lane == k - 1) sh.thr = mine ? mine + plus : 0;
     const int have = __popc(__ballot_sync(0xffffffffu, mine != 0));
@@ -211,7 +233,7 @@ __device__ __forceinline__ void lp_compact(LpShared& sh, int n, int k, int plus)
 // raise the bound when there are many, which an order that keeps rising makes
 // slower but not wrong.
 template <int DT, bool TOP>
-__global__ void __launch_bounds__(kLpThreads) k_token_logprobs(const __grid_constant__ LogprobParams a) {
+__global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(const __grid_constant__ LogprobParams a) {
   extern __shared__ __align__(16) unsigned char smem[];
   LpShared& sh = *reinterpret_cast<LpShared*>(smem);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -224,7 +246,8 @@ __global__ void __launch_bounds__(kLpThreads) k_token_logprobs(const __grid_cons
   const int v0 = c0 + pre, nv = (c1 - v0) / kVec, rest = (c1 - v0) - nv * kVec;
   const uint4* body = reinterpret_cast<const uint4*>(row + (size_t)v0 * kSize);
 
-  LpRegs<DT> cur, nxt;
+  constexpr int kAhead = DT == DT_F32 ? 1 : 2;  // steps in flight: 64 bytes a thread
+  LpRegs<DT> cur, nxt[kAhead];
   constexpr int kLoads = kLpEach / kVec;
   constexpr uint32_t kNegInf = DT == DT_F32 ? 0xff800000u : DT == DT_BF16 ? 0xff80ff80u : 0xfc00fc00u;
   auto load = [&](LpRegs<DT>& g, int at) {  // vectors at + j * 256 + t; -infinity behind the end
@@ -236,6 +259,8 @@ __global__ void __launch_bounds__(kLpThreads) k_token_logprobs(const __grid_cons
   };
   constexpr int kStepVec = kLpThreads * kLoads;
   load(cur, 0);
+#pragma unroll
+  for (int i = 0; i < kAhead - 1; ++i) load(nxt[i], (i + 1) * kStepVec);
 
   LpSum s = {-FLT_MAX, 0.f, 0.f};
   unsigned long long thr = 0;
@@ -264,12 +289,23 @@ __global__ void __launch_bounds__(kLpThreads) k_token_logprobs(const __grid_cons
     if (TOP) candidate(x, i);
   }
   for (int at = 0; at < nv; at += kStepVec) {
-    if (at + kStepVec < nv) load(nxt, at + kStepVec);
+    if (at + kAhead * kStepVec < nv) load(nxt[kAhead - 1], at + kAhead * kStepVec);
     const float mx = cur.largest();
     if (mx > s.m) s.raise(mx);
-    const float nm = -s.m;
+    {
+      const float nm = -s.m;
+      float2 z = make_float2(0.f, 0.f), e2 = z;
 #pragma unroll
-    for (int i = 0; i < kLpEach; ++i) s.add_diff(cur.diff(i, nm));
+      for (int i = 0; i < kLpEach; i += 2) {
+        const float2 y = make_float2(max_nan(cur.diff(i, nm), kLpFar) * kLog2e,
+                                     max_nan(cur.diff(i + 1, nm), kLpFar) * kLog2e);
+        const float2 e = make_float2(lp_exp2(y.x), lp_exp2(y.y));
+        z = add2(z, e);
+        e2 = fma2(e, y, e2);
+      }
+      s.z += z.x + z.y;
+      s.t += e2.x + e2.y;
+    }
     if (TOP) {
       if (at == 0) {
         // the threads' best values, over what the candidates will hold
@@ -312,34 +348,24 @@ __global__ void __launch_bounds__(kLpThreads) k_token_logprobs(const __grid_cons
         __syncthreads();
       }
     }
-    cur = nxt;
+    cur = nxt[0];
+#pragma unroll
+    for (int i = 1; i < kAhead; ++i) nxt[i - 1] = nxt[i];
   }
   if (TOP) {
     __syncthreads();
     lp_compact(sh, sh.n, a.k, 1);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    LpSum p;
-    p.m = __shfl_xor_sync(0xffffffffu, s.m, o);
-    p.z = __shfl_xor_sync(0xffffffffu, s.z, o);
-    p.t = __shfl_xor_sync(0xffffffffu, s.t, o);
-    // the same order on both sides, so that the lanes agree to the bit
-    if (lane & o) {
-      p.join(s);
-      s = p;
-    } else {
-      s.join(p);
-    }
-  }
+  s.join_lanes(32);
   if (lane == 0) sh.sums[warp] = s;
   __syncthreads();
+  if (warp == 0) {
+    s = sh.sums[lane & (kLpWarps - 1)];
+    s.join_lanes(kLpWarps);
+  }
   if (a.splits > 1) {
     const size_t at = (size_t)r * a.splits;
-    if (t == 0) {
-      for (int w = 1; w < kLpWarps; ++w) s.join(sh.sums[w]);
-      a.stat[at + sp] = make_float4(s.m, s.z, s.t, 0.f);
-    }
+    if (t == 0) a.stat[at + sp] = make_float4(s.m, s.z, s.t, 0.f);
     if (TOP && t < a.k) a.keys[(at + sp) * a.k + t] = sh.buf[t];
     __syncthreads();
     if (t == 0) {
@@ -352,29 +378,27 @@ __global__ void __launch_bounds__(kLpThreads) k_token_logprobs(const __grid_cons
     if (!sh.last) return;
     // the row's last CTA: the splits' sums in their order, and the best of
     // their best
+    if (warp == 0) {
+      static_assert(kLpSplits == 64, "two splits a lane");
+      const float4 v = lane < a.splits ? __ldcg(a.stat + at + lane) : make_float4(-FLT_MAX, 0.f, 0.f, 0.f);
+      const float4 w =
+          lane + 32 < a.splits ? __ldcg(a.stat + at + lane + 32) : make_float4(-FLT_MAX, 0.f, 0.f, 0.f);
+      s = {v.x, v.y, v.z};
+      s.join({w.x, w.y, w.z});
+      s.join_lanes(32);
+    }
     if (TOP) {
       const int n = a.splits * a.k;
       for (int i = t; i < n; i += kLpThreads) sh.buf[i] = __ldcg(a.keys + at * a.k + i);
       __syncthreads();
       lp_compact(sh, n, a.k, 1);
     }
-    if (t == 0) {
-      float4 v = __ldcg(a.stat + at);
-      s = {v.x, v.y, v.z};
-      for (int i = 1; i < a.splits; ++i) {
-        v = __ldcg(a.stat + at + i);
-        s.join({v.x, v.y, v.z});
-      }
-    }
-  } else if (t == 0) {
-    for (int w = 1; w < kLpWarps; ++w) s.join(sh.sums[w]);
   }
-  if (t == 0) sh.sums[0] = s;
-  __syncthreads();
-  s = sh.sums[0];
+  if (warp > 0) return;
+  // the alternatives are at most 32: one a lane of the first warp
   const float lz = logf(s.z);
   if (t == 0) {
-    if (a.entropy) a.entropy[r] = lz - s.t / s.z;
+    if (a.entropy) a.entropy[r] = lz - s.t / s.z / kLog2e;
     if (a.targets) {
       const int i = a.targets[r];
       float lp = 0.f;
@@ -403,7 +427,7 @@ __global__ void __launch_bounds__(kLpThreads) k_token_logprobs(const __grid_cons
 static void lp_split(int rows, int V, int& splits, int& chunk) {
   const int steps = (V + kLpStep - 1) / kLpStep;
   int want = kLpCtas / rows;
-  if (want > 64) want = 64;
+  if (want > kLpSplits) want = kLpSplits;
   if (want < 1) want = 1;
   const int per = (steps + want - 1) / want;
   chunk = per * kLpStep;
