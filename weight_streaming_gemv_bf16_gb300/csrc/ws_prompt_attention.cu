@@ -1,86 +1,537 @@
 // ws_prompt_attention.cu -- causal attention over packed prompts with grouped
 // heads: token t of a sequence attends to the sequence's tokens up to t.
 //
-// out = sum_j p_j v_j, p = softmax_j(q . k_j / sqrt(128)).
+// out = sum_j p_j v_j, p = softmax_j(q . k_j / sqrt(128)); one pass over the
+// keys with a running maximum m and sum l: p_j = 2^(c s_j - m), l = sum p_j,
+// out = sum p_j v_j / l, c = log2(e) / sqrt(128).  m follows the keys' maximum
+// only when that is 2^8 above it, so the output accumulators are rarely
+// rescaled and a p is at most 2^8.
+//
+// One CTA takes two tiles of 128 query rows that read the same keys and
+// values: two heads of one group over the same tokens where the group is even,
+// else two neighbouring runs of tokens of one head.  Twelve warps:
+//   0..3, 4..7  the softmax of tile 0 and of tile 1, a thread a row: scores out
+//               of tensor memory, probabilities back into it over the scores;
+//   8           issues the products (one thread): S = Q K^T from shared memory,
+//               O += P V with P from tensor memory, both accumulators there
+//               (S, S, O, O: the 512 columns); while one tile's softmax runs,
+//               the tensor cores work for the other;
+//   9           the copies: Q once, K and V through two stages each;
+//   10, 11      guard the values of the last blocks, where keys are masked: a
+//               probability of 0 times a value that is not finite would still
+//               be NaN, so those values, and the rows behind the sequence, are
+//               zeroed in shared memory before the product, and the rows that
+//               do attend to such a value get its share at the end.
 #include <cmath>
+#include <mutex>
 
 #include "ws_kv_q4.cuh"
+#include "ws_tcgen05.cuh"
 
 #include "wsgemv.h"
 
 namespace ws {
 
 constexpr int kPromptDim = 128;
+constexpr int kPaTile = 128;                       // query rows a tile, keys a block
+constexpr int kPaThreads = 384;
+constexpr int kPaTileBytes = kPaTile * kPromptDim * 2;
+constexpr int kPaHalf = kPaTileBytes / 2;          // 128 rows of 64 values, 128-byte swizzle
+constexpr int kPaStages = 2;                       // of keys, and of values
+constexpr int kPaSmem = (2 + 2 * kPaStages) * kPaTileBytes + 1024;
+constexpr float kPaLazy = 8.f;
+constexpr int kPaRegsSoftmax = 216, kPaRegsOther = 72;
+static_assert(256 * kPaRegsSoftmax + 128 * kPaRegsOther <= kPaThreads * 168,
+              "the register shares fit what the block is launched with");
 
 struct PromptParams {
-  const uint16_t* q;  // [T][nh][128], token strides in elements
-  const uint16_t* k;  // [T][nkv][128]
+  CUtensorMap mq, mk, mv;  // [T][heads][128], boxes of 128 tokens x 64 dimensions
+  const uint16_t* q;       // the same, for the rows that need single values
+  const uint16_t* k;
   const uint16_t* v;
-  const int* cu;      // [n + 1]
-  uint16_t* out;      // [T][nh * 128]
-  float* lse;         // [T][nh] or null
+  const int* cu;           // [n + 1]
+  uint16_t* out;           // [T][nh * 128]
+  float* lse;              // [T][nh] or null
   long long qs, ks, vs;
   int T, n, nh, nkv;
-  float scale;
+  int pair;                // 1: the tiles are two heads; 0: two runs of one head
+  float scale;             // log2(e) / sqrt(128)
   int* err;
+  unsigned long long timeout_ns;
 };
 
-// One warp per (token, head), four dimensions a lane, the keys one by one.
-template <int DT>
-__global__ void __launch_bounds__(128) k_prompt_attention(const __grid_constant__ PromptParams a) {
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 5), h = blockIdx.y, lane = threadIdx.x & 31;
-  if (blockIdx.x == 0 && h == 0)
-    for (int i = threadIdx.x; i < a.n; i += 128)
-      if (a.cu[i] < 0 || a.cu[i + 1] < a.cu[i] || a.cu[i + 1] > a.T) atomicExch(a.err, kDerrBadSeq);
-  if (t >= a.T) return;
-  int lo = 0, hi = a.n;
-  if (a.cu[0] > t) return;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.cu[mid] <= t) lo = mid; else hi = mid - 1;
+struct PaShared {
+  uint64_t q_full[2], k_full[kPaStages], k_empty[kPaStages], v_full[kPaStages], v_empty[kPaStages];
+  uint64_t s_full[2], p_full[2], o_full[2], guard_go[2], guard[2], drain;
+  uint32_t tmem;
+  uint32_t odd[2][4];      // values of the guarded blocks that are not finite, a bit a key
+  int abort;
+};
+
+__device__ __forceinline__ float pa_exp2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Wait with the library's limit; a wait that runs out ends every other one.
+__device__ __forceinline__ bool pa_wait_slow(uint64_t* bar, uint32_t parity, PaShared* sh, int* err,
+                                          unsigned long long timeout_ns) {
+  const uint64_t t0 = global_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*(volatile int*)&sh->abort) return false;
+    if (global_ns() - t0 > timeout_ns) {
+      *(volatile int*)&sh->abort = 1;
+      atomicExch(err, (int)DERR_TIMEOUT);
+      return false;
+    }
   }
-  if (lo >= a.n || a.cu[lo + 1] <= t) return;
-  const int j0 = a.cu[lo], g = h / (a.nh / a.nkv);
-  if (j0 < 0 || a.cu[lo + 1] > a.T) return;
-  auto get = [&](const uint16_t* p, long long stride, int tok, int head, float (&x)[4]) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p + (size_t)tok * stride +
-                                                    (size_t)head * kPromptDim + lane * 4);
-    const uint32_t w[2] = {u.x, u.y};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if constexpr (DT == DT_F16) {
-        const __half2 y = *reinterpret_cast<const __half2*>(&w[i]);
-        x[2 * i] = __low2float(y);
-        x[2 * i + 1] = __high2float(y);
-      } else {
-        x[2 * i] = bf16lo(w[i]);
-        x[2 * i + 1] = bf16hi(w[i]);
+}
+__device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, PaShared* sh,
+                                        const PromptParams& a) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return pa_wait_slow(bar, parity, sh, a.err, a.timeout_ns);
+}
+
+// Sequence and query block of tile `t` (units of `rows` tokens), by the whole
+// warp: the tiles with the most keys first, whatever their sequence, while the
+// bounds fit the lanes; sequence by sequence beyond that.  false: no such tile.
+__device__ __forceinline__ bool pa_place(const PromptParams& a, int t, int rows, int& first,
+                                         int& len, int& block) {
+  const int lane = threadIdx.x & 31;
+  const unsigned all = 0xffffffffu;
+  for (int b0 = 0; b0 < a.n; b0 += 32) {
+    const int i = b0 + lane;
+    int lo = 0, hi = 0;
+    if (i < a.n) {
+      lo = a.cu[i];
+      hi = a.cu[i + 1];
+      if (lo < 0 || hi < lo || hi > a.T) {
+        if (blockIdx.x == 0 && threadIdx.x < 32) atomicExch(a.err, kDerrBadSeq);
+        lo = hi = 0;
       }
     }
-  };
-  float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-  get(a.q, a.qs, t, h, q);
-  for (int j = j0; j <= t; ++j) {
-    float k[4], v[4];
-    get(a.k, a.ks, j, g, k);
-    get(a.v, a.vs, j, g, v);
-    const float s = warp_sum(q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3]) * a.scale;
-    const float mn = s == -INFINITY ? m : fmaxf(m, s);
-    const float f = m == mn ? 1.f : expf(m - mn);
-    const float p = s == -INFINITY ? 0.f : expf(s - mn);
-    m = mn;
-    l = l * f + p;
+    const int nt = (hi - lo + rows - 1) / rows;
+    const int total = __reduce_add_sync(all, nt);
+    if (t >= total) {
+      t -= total;
+      continue;
+    }
+    int src;
+    if (a.n <= 32) {
+      // tiles of block b and up: sum max(0, nt - b); the largest b with more than t
+      int lo_b = 0, hi_b = __reduce_max_sync(all, nt);
+      while (hi_b - lo_b > 1) {
+        const int mid = (lo_b + hi_b) >> 1;
+        if (__reduce_add_sync(all, max(0, nt - mid)) > t) lo_b = mid; else hi_b = mid;
+      }
+      block = lo_b;
+      const int rank = t - __reduce_add_sync(all, max(0, nt - block - 1));
+      unsigned m = __ballot_sync(all, nt > block);
+      for (int k = 0; k < rank; ++k) m &= m - 1;
+      src = __ffs(m) - 1;
+    } else {
+      int sum = nt;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = fmaf(p, v[i], o[i] * f);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(all, sum, o);
+        if (lane >= o) sum += u;
+      }
+      src = __ffs(__ballot_sync(all, sum > t)) - 1;
+      block = __shfl_sync(all, sum, src) - 1 - t;
+    }
+    first = __shfl_sync(all, lo, src);
+    len = __shfl_sync(all, hi, src) - first;
+    return true;
   }
-  uint16_t* out = a.out + ((size_t)t * a.nh + h) * kPromptDim + lane * 4;
+  return false;
+}
+
+template <int DT>
+__device__ __forceinline__ float pa_value(const uint16_t* p) {
+  return DT == DT_F16 ? __half2float(__ushort_as_half(*p)) : __uint_as_float((uint32_t)*p << 16);
+}
+template <int DT>
+__device__ __forceinline__ uint32_t pa_pack(float lo, float hi) {
+  if constexpr (DT == DT_F16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// The share of the guarded values that are not finite in 32 dimensions of one
+// row's accumulators: p times the value for each that the row attends to.
+template <int DT>
+__device__ __forceinline__ void pa_odd_values(const PromptParams& a, const PaShared* sh, int first,
+                                           int tok, int guard0, int head, int kvh, float m, int d0,
+                                           uint32_t* o) {
+  for (int e = 0; e < 2; ++e)
+    for (int w = 0; w < 4; ++w) {
+      uint32_t bits = sh->odd[e][w];
+      while (bits) {
+        const int key = (guard0 + e) * kPaTile + w * 32 + __ffs(bits) - 1;
+        bits &= bits - 1;
+        if (key > tok) continue;
+        const uint16_t* q = a.q + (size_t)(first + tok) * a.qs + (size_t)head * kPromptDim;
+        const uint16_t* k = a.k + (size_t)(first + key) * a.ks + (size_t)kvh * kPromptDim;
+        const uint16_t* v = a.v + (size_t)(first + key) * a.vs + (size_t)kvh * kPromptDim + d0;
+        float s = 0.f;
+        for (int d = 0; d < kPromptDim; ++d) s = fmaf(pa_value<DT>(q + d), pa_value<DT>(k + d), s);
+        const float p = pa_exp2(fmaf(s, a.scale, -m));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float v = o[i] / l;
-    out[i] = DT == DT_F16 ? __half_as_ushort(__float2half_rn(v))
-                          : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+        for (int d = 0; d < 32; ++d)
+          o[d] = __float_as_uint(fmaf(p, pa_value<DT>(v + d), __uint_as_float(o[d])));
+      }
+    }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kPaThreads, 1)
+    k_prompt_attention(const __grid_constant__ PromptParams a) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ PaShared sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int heads = a.pair ? a.nh / 2 : a.nh, rows = a.pair ? kPaTile : 2 * kPaTile;
+  int first, len, block;
+  if (!pa_place(a, blockIdx.x / heads, rows, first, len, block)) return;
+  const int h0 = (blockIdx.x % heads) * (a.pair ? 2 : 1), kvh = h0 / (a.nh / a.nkv);
+  // per tile: head, first row of the sequence, blocks of keys (0: no tile)
+  const int row0 = block * rows, row1 = a.pair ? row0 : row0 + kPaTile;
+  const int n0 = row0 / kPaTile + 1, n1 = row1 < len ? row1 / kPaTile + 1 : 0;
+  const int nb = max(n0, n1), guard0 = n0 - 1;  // the blocks from guard0 on hold masked keys
+
+  unsigned char* smem = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  unsigned char* sq = smem;
+  unsigned char* sk = smem + 2 * kPaTileBytes;
+  unsigned char* sv = sk + kPaStages * kPaTileBytes;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 128);
+      mbar_init(&sh.o_full[i], 1);
+      mbar_init(&sh.guard_go[i], 1);
+      mbar_init(&sh.guard[i], 64);
+    }
+    for (int i = 0; i < kPaStages; ++i) {
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.v_full[i], 1);
+      mbar_init(&sh.v_empty[i], 1);
+    }
+    mbar_init(&sh.drain, 1);
+    fence_mbar_init();
+    sh.abort = 0;
   }
-  if (a.lse && lane == 0) a.lse[(size_t)t * a.nh + h] = m + logf(l);
+  if (threadIdx.x < 8) sh.odd[threadIdx.x >> 2][threadIdx.x & 3] = 0;
+  if (warp == 8) tmem_alloc(&sh.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  if (warp < 8) {
+    regs_raise<kPaRegsSoftmax>();
+    const int tile = warp >> 2, r = (warp & 3) * 32 + lane;
+    const int n = tile ? n1 : n0, head = h0 + (a.pair ? tile : 0);
+    const int tok = (tile ? row1 : row0) + r;  // of the sequence
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + tile * 128 + lanes, to = tmem + 256 + tile * 128 + lanes;
+    float m = -1e30f;
+    float2 l = make_float2(0.f, 0.f);
+    bool ok = true;
+    for (int j = 0; j < n && ok; ++j) {
+      ok = pa_wait(&sh.s_full[tile], j & 1, &sh, a);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s + 32 * c);
+      tmem_wait_ld();
+      if (j == n - 1) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c > r) s[c] = 0xff800000u;
+      }
+      float mx[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
+#pragma unroll
+      for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale;
+      if (__any_sync(0xffffffffu, top > m + kPaLazy)) {
+        const float mn = fmaxf(m, top), f = pa_exp2(m - mn);
+        m = mn;
+        l.x *= f, l.y *= f;
+        if (j > 0) {  // the products up to block j - 1 are done: this block's scores came after
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(to + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st32(to + c, o);
+          }
+        }
+      }
+      const float2 sc = make_float2(a.scale, a.scale), nm = make_float2(-m, -m);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t p[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float2 x = make_float2(__uint_as_float(s[64 * h + 2 * i]), __uint_as_float(s[64 * h + 2 * i + 1]));
+          x = fma2(x, sc, nm);
+          x.x = pa_exp2(x.x);
+          x.y = pa_exp2(x.y);
+          l = add2(l, x);
+          p[i] = pa_pack<DT>(x.x, x.y);
+        }
+        tmem_st32(ts + 32 * h, p);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&sh.p_full[tile]);
+    }
+    if (n > 0 && ok) ok = __all_sync(0xffffffffu, pa_wait(&sh.o_full[tile], 0, &sh, a));
+    if (n > 0 && ok) {
+      tc_fence_after();
+      const float sum = l.x + l.y, inv = 1.f / sum;
+      const uint32_t odd = sh.odd[0][0] | sh.odd[0][1] | sh.odd[0][2] | sh.odd[0][3] |
+                           sh.odd[1][0] | sh.odd[1][1] | sh.odd[1][2] | sh.odd[1][3];
+      // rows to the tile's query buffer (its products are done), 16-byte
+      // pieces in an order that spreads over the banks, then out row by row
+      unsigned char* st = sq + tile * kPaTileBytes + (warp & 3) * 32 * 256;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        tmem_ld32(to + 32 * c, o);
+        tmem_wait_ld();
+        if (odd && tok < len) pa_odd_values<DT>(a, &sh, first, tok, guard0, head, kvh, m, 32 * c, o);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pa_pack<DT>(__uint_as_float(o[8 * i + 2 * e]) * inv,
+                               __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+          const int piece = (4 * c + i) ^ (lane & 7);
+          *reinterpret_cast<uint4*>(st + lane * 256 + piece * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      if (a.lse && tok < len)
+        a.lse[(size_t)(first + tok) * a.nh + head] = (m + log2f(sum)) * 0.6931471805599453f;
+      __syncwarp();
+      const int base = tok - lane;  // the warp's first row
+#pragma unroll 4
+      for (int i = 0; i < 16; ++i) {
+        const int rr = 2 * i + (lane >> 4), piece = lane & 15;
+        if (base + rr < len)
+          *reinterpret_cast<uint4*>(a.out + ((size_t)(first + base + rr) * a.nh + head) * kPromptDim +
+                                    piece * 8) =
+              *reinterpret_cast<const uint4*>(st + rr * 256 + (piece ^ (rr & 7)) * 16);
+      }
+    }
+  } else {
+    regs_lower<kPaRegsOther>();
+    if (warp == 8) {
+      if (lane == 0) {
+        constexpr uint32_t qk = mma_idesc(DT == DT_BF16, false, kPaTile, kPaTile);
+        constexpr uint32_t pv = mma_idesc(DT == DT_BF16, true, kPaTile, kPromptDim);
+        bool ok = true;
+        auto scores = [&](int tile, int j) {  // S = Q K^T, 16 dimensions at a time
+          const uint32_t q = smem_addr(sq + tile * kPaTileBytes);
+          const uint32_t k = smem_addr(sk + (j % kPaStages) * kPaTileBytes);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t at = (i >> 2) * kPaHalf + (i & 3) * 32;
+            mma_ss(tmem + tile * 128, smem_desc(q + at, 16, 1024), smem_desc(k + at, 16, 1024), qk, i > 0);
+          }
+          mma_commit(&sh.s_full[tile]);
+        };
+        auto values = [&](int tile, int j) {  // O += P V, 16 keys at a time
+          const uint32_t v = smem_addr(sv + (j % kPaStages) * kPaTileBytes);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            mma_ts(tmem + 256 + tile * 128, tmem + tile * 128 + i * 8,
+                   smem_desc(v + i * 2048, kPaHalf, 1024), pv, j > 0 || i > 0);
+        };
+        const int nt[2] = {n0, n1};
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          if (ok) ok = pa_wait(bar, parity, &sh, a);
+        };
+        wait(&sh.k_full[0], 0);
+        for (int i = 0; i < 2; ++i)
+          if (nt[i] > 0) {
+            wait(&sh.q_full[i], 0);
+            if (ok) scores(i, 0);
+          }
+        if (ok && kPaStages < nb) mma_commit(&sh.k_empty[0]);
+        for (int j = 0; j < nb && ok; ++j) {
+          const int s = j % kPaStages, s1 = (j + 1) % kPaStages;
+          wait(&sh.v_full[s], (j / kPaStages) & 1);
+          if (j >= guard0) wait(&sh.guard[j - guard0], 0);
+          for (int i = 0; i < 2; ++i) {
+            if (j >= nt[i]) continue;
+            wait(&sh.p_full[i], j & 1);
+            if (!ok) break;
+            tc_fence_after();
+            values(i, j);
+            if (j + 1 < nt[i]) {
+              wait(&sh.k_full[s1], ((j + 1) / kPaStages) & 1);
+              if (ok) scores(i, j + 1);
+            } else {
+              mma_commit(&sh.o_full[i]);
+            }
+          }
+          if (ok) {
+            // stages that are filled again
+            if (j + kPaStages < nb) mma_commit(&sh.v_empty[s]);
+            if (j + 1 + kPaStages < nb) mma_commit(&sh.k_empty[s1]);
+          }
+        }
+        // after a wait that ran out: nothing of this CTA stays in flight
+        if (!ok) {
+          mma_commit(&sh.drain);
+          mbar_wait_bounded(&sh.drain, 0, a.timeout_ns);
+        }
+      }
+    } else if (warp == 9) {
+      if (lane == 0) {
+        bool ok = true;
+        auto tile = [&](unsigned char* dst, const CUtensorMap* map, int h, int tok, uint64_t* bar) {
+          mbar_arrive_expect_tx(bar, kPaTileBytes);
+          tma_load_3d(dst, map, 0, h, tok, bar);
+          tma_load_3d(dst + kPaHalf, map, 64, h, tok, bar);
+        };
+        tile(sq, &a.mq, h0, first + row0, &sh.q_full[0]);
+        int j = 0;
+        for (; j < nb; ++j) {
+          const int s = j % kPaStages;
+          const uint32_t par = (j / kPaStages + 1) & 1;
+          if (j >= kPaStages) ok = pa_wait(&sh.k_empty[s], par, &sh, a);
+          if (!ok) break;
+          tile(sk + s * kPaTileBytes, &a.mk, kvh, first + j * kPaTile, &sh.k_full[s]);
+          if (j == 0 && n1 > 0)
+            tile(sq + kPaTileBytes, &a.mq, h0 + a.pair, first + row1, &sh.q_full[1]);
+          if (j >= kPaStages) ok = pa_wait(&sh.v_empty[s], par, &sh, a);
+          if (!ok) break;
+          tile(sv + s * kPaTileBytes, &a.mv, kvh, first + j * kPaTile, &sh.v_full[s]);
+          // from here on the stage's phase is this block's
+          if (j >= guard0) mbar_arrive(&sh.guard_go[j - guard0]);
+        }
+        if (!ok) {  // the copies that are still under way
+          mbar_wait_bounded(&sh.q_full[0], 0, a.timeout_ns);
+          if (n1 > 0) mbar_wait_bounded(&sh.q_full[1], 0, a.timeout_ns);
+          for (int i = max(0, j - kPaStages); i <= j; ++i) {
+            if (i < j || i == nb) mbar_wait_bounded(&sh.v_full[i % kPaStages], (i / kPaStages) & 1, a.timeout_ns);
+            mbar_wait_bounded(&sh.k_full[i % kPaStages], (i / kPaStages) & 1, a.timeout_ns);
+          }
+        }
+      }
+    } else {
+      const int t = (warp - 10) * 32 + lane;
+      for (int j = guard0; j < nb; ++j) {
+        const int s = j % kPaStages;
+        if (!pa_wait(&sh.guard_go[j - guard0], 0, &sh, a) ||
+            !pa_wait(&sh.v_full[s], (j / kPaStages) & 1, &sh, a))
+          break;
+        const int valid = len - j * kPaTile;  // keys of the block inside the sequence
+#pragma unroll 1
+        for (int key = t; key < kPaTile; key += 64) {
+          uint4* half0 = reinterpret_cast<uint4*>(sv + s * kPaTileBytes + key * 128);
+          uint4* half1 = reinterpret_cast<uint4*>(sv + s * kPaTileBytes + kPaHalf + key * 128);
+          bool zero = key >= valid;
+          if (!zero) {
+            uint32_t bad = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint4 u = i < 8 ? half0[i] : half1[i - 8];
+              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+              // an exponent of all ones carries into the sign's place
+              constexpr uint32_t kExp = DT == DT_F16 ? 0x7c007c00u : 0x7f807f80u;
+              constexpr uint32_t kOne = DT == DT_F16 ? 0x04000400u : 0x00800080u;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) bad |= (w[e] & kExp) + kOne;
+            }
+            zero = (bad & 0x80008000u) != 0;
+            if (zero) atomicOr(&sh.odd[j - guard0][key >> 5], 1u << (key & 31));
+          }
+          if (zero) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) half0[i] = half1[i] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_proxy_async_smem();  // what was zeroed before the product reads it
+        mbar_arrive(&sh.guard[j - guard0]);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+typedef CUresult (*PaEncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                               const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder, and the kernels' attribute, once per device.
+static PaEncodeFn pa_setup(cudaError_t* err) {
+  constexpr int kMaxDev = 64;
+  static std::mutex mu;
+  static PaEncodeFn fn = nullptr;
+  static bool ready[kMaxDev] = {false};
+  int dev = 0;
+  *err = cudaGetDevice(&dev);
+  if (*err == cudaSuccess && (dev < 0 || dev >= kMaxDev)) *err = cudaErrorInvalidDevice;
+  if (*err != cudaSuccess) return nullptr;
+  std::lock_guard<std::mutex> lk(mu);
+  if (!fn) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    *err = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                            cudaEnableDefault, &q);
+    if (*err == cudaSuccess && q != cudaDriverEntryPointSuccess) *err = cudaErrorNotSupported;
+    if (*err != cudaSuccess) return nullptr;
+    fn = reinterpret_cast<PaEncodeFn>(ptr);
+  }
+  if (!ready[dev]) {
+    *err = cudaFuncSetAttribute(k_prompt_attention<DT_BF16>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kPaSmem);
+    if (*err == cudaSuccess)
+      *err = cudaFuncSetAttribute(k_prompt_attention<DT_F16>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kPaSmem);
+    if (*err != cudaSuccess) return nullptr;
+    ready[dev] = true;
+  }
+  return fn;
+}
+
+static bool pa_map(PaEncodeFn fn, CUtensorMap* map, int dtype, const void* base, int T, int heads,
+                   long long stride) {
+  const cuuint64_t dims[3] = {(cuuint64_t)kPromptDim, (cuuint64_t)heads, (cuuint64_t)T};
+  const cuuint64_t strides[2] = {kPromptDim * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {kPromptDim / 2, 1, kPaTile};
+  const cuuint32_t step[3] = {1, 1, 1};
+  return fn(map, dtype == WS_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+            3, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace ws
@@ -116,6 +567,26 @@ ws_status ws_prompt_attention(const void *q, const void *k, const void *v, int d
     return WS_ERR_ALIGN;
   }
   PromptParams a = {};
+  a.pair = (n_heads / n_kv_heads) % 2 == 0;
+  // at most: the tokens' whole tiles, and one more a sequence
+  const long long rows = a.pair ? kPaTile : 2 * kPaTile;
+  const long long tiles = T / rows + n_seqs, grid = tiles * (a.pair ? n_heads / 2 : n_heads);
+  if (grid > 0x7fffffffll || T > 0x7fffffff - 2 * kPaTile) {
+    set_error("prompt attention: too many tiles (%lld)", grid);
+    return WS_ERR_SHAPE;
+  }
+  cudaError_t e = cudaSuccess;
+  const PaEncodeFn fn = pa_setup(&e);
+  if (!fn) {
+    set_error("prompt attention setup failed: %s", cudaGetErrorString(e));
+    return WS_ERR_CUDA;
+  }
+  if (!pa_map(fn, &a.mq, dtype, q, T, n_heads, q_stride) ||
+      !pa_map(fn, &a.mk, dtype, k, T, n_kv_heads, k_stride) ||
+      !pa_map(fn, &a.mv, dtype, v, T, n_kv_heads, v_stride)) {
+    set_error("prompt attention: tensor map encoding failed");
+    return WS_ERR_CUDA;
+  }
   a.q = static_cast<const uint16_t*>(q);
   a.k = static_cast<const uint16_t*>(k);
   a.v = static_cast<const uint16_t*>(v);
@@ -129,18 +600,18 @@ ws_status ws_prompt_attention(const void *q, const void *k, const void *v, int d
   a.n = n_seqs;
   a.nh = n_heads;
   a.nkv = n_kv_heads;
-  a.scale = 1.0f / sqrtf((float)kPromptDim);
+  a.scale = (float)(1.4426950408889634 / sqrt((double)kPromptDim));
+  a.timeout_ns = tuning().timeout_ns;
   a.err = device_error_ptr();
   if (!a.err) {
     set_error("device error flag unavailable");
     return WS_ERR_CUDA;
   }
-  const dim3 grid((T + 3) / 4, n_heads);
   if (dtype == WS_DTYPE_F16)
-    k_prompt_attention<DT_F16><<<grid, 128, 0, (cudaStream_t)stream>>>(a);
+    k_prompt_attention<DT_F16><<<(int)grid, kPaThreads, kPaSmem, (cudaStream_t)stream>>>(a);
   else
-    k_prompt_attention<DT_BF16><<<grid, 128, 0, (cudaStream_t)stream>>>(a);
-  const cudaError_t e = cudaGetLastError();
+    k_prompt_attention<DT_BF16><<<(int)grid, kPaThreads, kPaSmem, (cudaStream_t)stream>>>(a);
+  e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("launch failed: %s", cudaGetErrorString(e));
     return WS_ERR_CUDA;
