@@ -9,15 +9,16 @@
 //
 // One CTA takes two tiles of 128 query rows that read the same keys and
 // values: two heads of one group over the same tokens where the group is even,
-// else two neighbouring runs of tokens of one head.  Twelve warps:
+// else two neighbouring runs of tokens of one head.  Sixteen warps:
 //   0..3, 4..7  the softmax of tile 0 and of tile 1, a thread a row: scores out
 //               of tensor memory, probabilities back into it over the scores;
-//   8           issues the products (one thread): S = Q K^T from shared memory,
-//               O += P V with P from tensor memory, both accumulators there
-//               (S, S, O, O: the 512 columns); while one tile's softmax runs,
-//               the tensor cores work for the other;
-//   9           the copies: Q once, K and V through two stages each;
-//   10, 11      guard the values of the last blocks, where keys are masked: a
+//   8, 9        issue the products of tile 0 and of tile 1 (one thread each): S =
+//               Q K^T from shared memory, O += P V with P from tensor memory,
+//               both accumulators there (S, S, O, O: the 512 columns).  The
+//               tensor cores take a product when they begin it, not before, so
+//               one thread for both tiles leaves them idle while it waits;
+//   10          the copies: Q once, K and V through two stages each;
+//   12..15      guard the values of the last blocks, where keys are masked: a
 //               probability of 0 times a value that is not finite would still
 //               be NaN, so those values, and the rows behind the sequence, are
 //               zeroed in shared memory before the product, and the rows that
@@ -34,14 +35,16 @@ namespace ws {
 
 constexpr int kPromptDim = 128;
 constexpr int kPaTile = 128;                       // query rows a tile, keys a block
-constexpr int kPaThreads = 384;
+constexpr int kPaThreads = 512;
 constexpr int kPaTileBytes = kPaTile * kPromptDim * 2;
 constexpr int kPaHalf = kPaTileBytes / 2;          // 128 rows of 64 values, 128-byte swizzle
 constexpr int kPaStages = 2;                       // of keys, and of values
 constexpr int kPaSmem = (2 + 2 * kPaStages) * kPaTileBytes + 1024;
+constexpr int kPaParts = 2;                        // of a block's probabilities, handed over one by one
+constexpr int kPaPart = kPaTile / kPaParts;
 constexpr float kPaLazy = 8.f;
-constexpr int kPaRegsSoftmax = 216, kPaRegsOther = 72;
-static_assert(256 * kPaRegsSoftmax + 128 * kPaRegsOther <= kPaThreads * 168,
+constexpr int kPaRegsSoftmax = 216, kPaRegsOther = 40;
+static_assert(256 * kPaRegsSoftmax + 256 * kPaRegsOther <= kPaThreads * 128,
               "the register shares fit what the block is launched with");
 
 struct PromptParams {
@@ -62,7 +65,7 @@ struct PromptParams {
 
 struct PaShared {
   uint64_t q_full[2], k_full[kPaStages], k_empty[kPaStages], v_full[kPaStages], v_empty[kPaStages];
-  uint64_t s_full[2], p_full[2], o_full[2], guard_go[2], guard[2], drain;
+  uint64_t s_full[2], p_full[2][kPaParts], o_full[2], guard_go[2], guard[2], drain[2];
   uint32_t tmem;
   uint32_t odd[2][4];      // values of the guarded blocks that are not finite, a bit a key
   int abort;
@@ -215,18 +218,18 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 128);
+      for (int h = 0; h < kPaParts; ++h) mbar_init(&sh.p_full[i][h], 4);
       mbar_init(&sh.o_full[i], 1);
       mbar_init(&sh.guard_go[i], 1);
-      mbar_init(&sh.guard[i], 64);
+      mbar_init(&sh.guard[i], 128);
+      mbar_init(&sh.drain[i], 1);
     }
     for (int i = 0; i < kPaStages; ++i) {
       mbar_init(&sh.k_full[i], 1);
-      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.k_empty[i], n1 > 0 ? 2 : 1);  // both tiles are done with a stage
       mbar_init(&sh.v_full[i], 1);
-      mbar_init(&sh.v_empty[i], 1);
+      mbar_init(&sh.v_empty[i], n1 > 0 ? 2 : 1);
     }
-    mbar_init(&sh.drain, 1);
     fence_mbar_init();
     sh.abort = 0;
   }
@@ -252,21 +255,26 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      uint32_t s[128];
+      uint32_t s[128], mx[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s + 32 * c);
+      for (int c = 0; c < 4; ++c) tmem_ld32_max(ts + 32 * c, s + 32 * c, mx[c]);
       tmem_wait_ld();
-      if (j == n - 1) {
+      tmem_loaded<128>(s);
+      asm volatile("" : "+r"(mx[0]), "+r"(mx[1]), "+r"(mx[2]), "+r"(mx[3]));
+      if (j == n - 1) {  // the diagonal: keys after the row's token
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c > r) s[c] = 0xff800000u;
+        for (int c = 0; c < 4; ++c) {
+          float y = -INFINITY;
+#pragma unroll
+          for (int i = 32 * c; i < 32 * c + 32; ++i) {
+            if (i > r) s[i] = 0xff800000u;
+            y = fmaxf(y, __uint_as_float(s[i]));
+          }
+          mx[c] = __float_as_uint(y);
+        }
       }
-      float mx[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
-#pragma unroll
-      for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale;
+      const float top = fmaxf(fmaxf(__uint_as_float(mx[0]), __uint_as_float(mx[1])),
+                              fmaxf(__uint_as_float(mx[2]), __uint_as_float(mx[3]))) * a.scale;
       if (__any_sync(0xffffffffu, top > m + kPaLazy)) {
         const float mn = fmaxf(m, top), f = pa_exp2(m - mn);
         m = mn;
@@ -277,6 +285,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             uint32_t o[32];
             tmem_ld32(to + c, o);
             tmem_wait_ld();
+            tmem_loaded<32>(o);
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
             tmem_st32(to + c, o);
@@ -285,22 +294,24 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       }
       const float2 sc = make_float2(a.scale, a.scale), nm = make_float2(-m, -m);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t p[32];
+      for (int h = 0; h < kPaParts; ++h) {
+        uint32_t p[kPaPart / 2];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float2 x = make_float2(__uint_as_float(s[64 * h + 2 * i]), __uint_as_float(s[64 * h + 2 * i + 1]));
-          x = fma2(x, sc, nm);
+        for (int i = 0; i < kPaPart / 2; ++i) {
+          const int c = kPaPart * h + 2 * i;
+          float2 x = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc, nm);
           x.x = pa_exp2(x.x);
           x.y = pa_exp2(x.y);
           l = add2(l, x);
           p[i] = pa_pack<DT>(x.x, x.y);
         }
-        tmem_st32(ts + 32 * h, p);
+        if constexpr (kPaPart == 64) tmem_st32(ts + 32 * h, p);
+        else tmem_st16(ts + 16 * h, p);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[tile][h]);
       }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&sh.p_full[tile]);
     }
     if (n > 0 && ok) ok = __all_sync(0xffffffffu, pa_wait(&sh.o_full[tile], 0, &sh, a));
     if (n > 0 && ok) {
@@ -316,6 +327,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         uint32_t o[32];
         tmem_ld32(to + 32 * c, o);
         tmem_wait_ld();
+        tmem_loaded<32>(o);
         if (odd && tok < len) pa_odd_values<DT>(a, &sh, first, tok, guard0, head, kvh, m, 32 * c, o);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -343,70 +355,58 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     }
   } else {
     regs_lower<kPaRegsOther>();
-    if (warp == 8) {
-      if (lane == 0) {
+    if (warp < 10) {
+      const int tile = warp - 8, n = tile ? n1 : n0;
+      if (n > 0 && elect_one()) {
         constexpr uint32_t qk = mma_idesc(DT == DT_BF16, false, kPaTile, kPaTile);
         constexpr uint32_t pv = mma_idesc(DT == DT_BF16, true, kPaTile, kPromptDim);
+        const uint32_t ts = tmem + tile * 128, to = tmem + 256 + tile * 128;
+        const uint32_t q = smem_addr(sq + tile * kPaTileBytes);
         bool ok = true;
-        auto scores = [&](int tile, int j) {  // S = Q K^T, 16 dimensions at a time
-          const uint32_t q = smem_addr(sq + tile * kPaTileBytes);
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          if (ok) ok = pa_wait(bar, parity, &sh, a);
+        };
+        auto scores = [&](int j) {  // S = Q K^T, 16 dimensions at a time
           const uint32_t k = smem_addr(sk + (j % kPaStages) * kPaTileBytes);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint32_t at = (i >> 2) * kPaHalf + (i & 3) * 32;
-            mma_ss(tmem + tile * 128, smem_desc(q + at, 16, 1024), smem_desc(k + at, 16, 1024), qk, i > 0);
+            mma_ss(ts, smem_desc(q + at, 16, 1024), smem_desc(k + at, 16, 1024), qk, i > 0);
           }
           mma_commit(&sh.s_full[tile]);
-        };
-        auto values = [&](int tile, int j) {  // O += P V, 16 keys at a time
-          const uint32_t v = smem_addr(sv + (j % kPaStages) * kPaTileBytes);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            mma_ts(tmem + 256 + tile * 128, tmem + tile * 128 + i * 8,
-                   smem_desc(v + i * 2048, kPaHalf, 1024), pv, j > 0 || i > 0);
-        };
-        const int nt[2] = {n0, n1};
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-          if (ok) ok = pa_wait(bar, parity, &sh, a);
+          if (j + kPaStages < nb) mma_commit(&sh.k_empty[j % kPaStages]);  // filled again
         };
         wait(&sh.k_full[0], 0);
-        for (int i = 0; i < 2; ++i)
-          if (nt[i] > 0) {
-            wait(&sh.q_full[i], 0);
-            if (ok) scores(i, 0);
-          }
-        if (ok && kPaStages < nb) mma_commit(&sh.k_empty[0]);
-        for (int j = 0; j < nb && ok; ++j) {
+        wait(&sh.q_full[tile], 0);
+        if (ok) scores(0);
+        for (int j = 0; j < n && ok; ++j) {
           const int s = j % kPaStages, s1 = (j + 1) % kPaStages;
           wait(&sh.v_full[s], (j / kPaStages) & 1);
           if (j >= guard0) wait(&sh.guard[j - guard0], 0);
-          for (int i = 0; i < 2; ++i) {
-            if (j >= nt[i]) continue;
-            wait(&sh.p_full[i], j & 1);
+          if (j + 1 < n) wait(&sh.k_full[s1], ((j + 1) / kPaStages) & 1);
+          const uint32_t v = smem_addr(sv + s * kPaTileBytes);
+#pragma unroll
+          for (int h = 0; h < kPaParts; ++h) {  // O += P V, 16 keys at a time
+            wait(&sh.p_full[tile][h], j & 1);
             if (!ok) break;
             tc_fence_after();
-            values(i, j);
-            if (j + 1 < nt[i]) {
-              wait(&sh.k_full[s1], ((j + 1) / kPaStages) & 1);
-              if (ok) scores(i, j + 1);
-            } else {
-              mma_commit(&sh.o_full[i]);
-            }
+#pragma unroll
+            for (int i = h * (kPaPart / 16); i < (h + 1) * (kPaPart / 16); ++i)
+              mma_ts(to, ts + i * 8, smem_desc(v + i * 2048, kPaHalf, 1024), pv, j > 0 || i > 0);
           }
-          if (ok) {
-            // stages that are filled again
-            if (j + kPaStages < nb) mma_commit(&sh.v_empty[s]);
-            if (j + 1 + kPaStages < nb) mma_commit(&sh.k_empty[s1]);
-          }
+          if (!ok) break;
+          if (j + kPaStages < nb) mma_commit(&sh.v_empty[s]);
+          if (j + 1 < n) scores(j + 1);
+          else mma_commit(&sh.o_full[tile]);
         }
-        // after a wait that ran out: nothing of this CTA stays in flight
+        // after a wait that ran out: nothing of this thread's stays in flight
         if (!ok) {
-          mma_commit(&sh.drain);
-          mbar_wait_bounded(&sh.drain, 0, a.timeout_ns);
+          mma_commit(&sh.drain[tile]);
+          mbar_wait_bounded(&sh.drain[tile], 0, a.timeout_ns);
         }
       }
-    } else if (warp == 9) {
-      if (lane == 0) {
+    } else if (warp == 10) {
+      if (elect_one()) {
         bool ok = true;
         auto tile = [&](unsigned char* dst, const CUtensorMap* map, int h, int tok, uint64_t* bar) {
           mbar_arrive_expect_tx(bar, kPaTileBytes);
@@ -438,38 +438,35 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           }
         }
       }
-    } else {
-      const int t = (warp - 10) * 32 + lane;
+    } else if (warp >= 12) {
+      const int key = (warp - 12) * 32 + lane;
       for (int j = guard0; j < nb; ++j) {
         const int s = j % kPaStages;
         if (!pa_wait(&sh.guard_go[j - guard0], 0, &sh, a) ||
             !pa_wait(&sh.v_full[s], (j / kPaStages) & 1, &sh, a))
           break;
         const int valid = len - j * kPaTile;  // keys of the block inside the sequence
-#pragma unroll 1
-        for (int key = t; key < kPaTile; key += 64) {
-          uint4* half0 = reinterpret_cast<uint4*>(sv + s * kPaTileBytes + key * 128);
-          uint4* half1 = reinterpret_cast<uint4*>(sv + s * kPaTileBytes + kPaHalf + key * 128);
-          bool zero = key >= valid;
-          if (!zero) {
-            uint32_t bad = 0;
+        uint4* half0 = reinterpret_cast<uint4*>(sv + s * kPaTileBytes + key * 128);
+        uint4* half1 = reinterpret_cast<uint4*>(sv + s * kPaTileBytes + kPaHalf + key * 128);
+        bool zero = key >= valid;
+        if (!zero) {
+          uint32_t bad = 0;
+#pragma unroll 4
+          for (int i = 0; i < 8; ++i) {
+            const uint4 u = half0[i], x = half1[i];
+            const uint32_t w[8] = {u.x, u.y, u.z, u.w, x.x, x.y, x.z, x.w};
+            // an exponent of all ones carries into the sign's place
+            constexpr uint32_t kExp = DT == DT_F16 ? 0x7c007c00u : 0x7f807f80u;
+            constexpr uint32_t kOne = DT == DT_F16 ? 0x04000400u : 0x00800080u;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint4 u = i < 8 ? half0[i] : half1[i - 8];
-              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-              // an exponent of all ones carries into the sign's place
-              constexpr uint32_t kExp = DT == DT_F16 ? 0x7c007c00u : 0x7f807f80u;
-              constexpr uint32_t kOne = DT == DT_F16 ? 0x04000400u : 0x00800080u;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) bad |= (w[e] & kExp) + kOne;
-            }
-            zero = (bad & 0x80008000u) != 0;
-            if (zero) atomicOr(&sh.odd[j - guard0][key >> 5], 1u << (key & 31));
+            for (int e = 0; e < 8; ++e) bad |= (w[e] & kExp) + kOne;
           }
-          if (zero) {
+          zero = (bad & 0x80008000u) != 0;
+          if (zero) atomicOr(&sh.odd[j - guard0][key >> 5], 1u << (key & 31));
+        }
+        if (zero) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) half0[i] = half1[i] = make_uint4(0, 0, 0, 0);
-          }
+          for (int i = 0; i < 8; ++i) half0[i] = half1[i] = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();  // what was zeroed before the product reads it
         mbar_arrive(&sh.guard[j - guard0]);
