@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   extern __shared__ unsigned char smem_raw[];
   __shared__ PaShared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 10 && lane < 3) tma_prefetch_map(lane == 0 ? &a.mq : lane == 1 ? &a.mk : &a.mv);
   const int heads = a.pair ? a.nh / 2 : a.nh, rows = a.pair ? kPaTile : 2 * kPaTile;
   int first, len, block;
   if (!pa_place(a, blockIdx.x / heads, rows, first, len, block)) return;
@@ -214,7 +215,15 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   unsigned char* sk = smem + 2 * kPaTileBytes;
   unsigned char* sv = sk + kPaStages * kPaTileBytes;
 
-  if (threadIdx.x == 0) {
+  // a tile's rows of one head: two boxes of 64 dimensions
+  auto copy = [&](unsigned char* dst, const CUtensorMap* map, int h, int tok, uint64_t* bar) {
+    mbar_arrive_expect_tx(bar, kPaTileBytes);
+    tma_load_3d(dst, map, 0, h, tok, bar);
+    tma_load_3d(dst + kPaHalf, map, 64, h, tok, bar);
+  };
+  // the copies' warp starts the barriers and the first copies before the
+  // tensor memory is there
+  if (warp == 10 && elect_one()) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.s_full[i], 1);
@@ -232,6 +241,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     }
     fence_mbar_init();
     sh.abort = 0;
+    copy(sq, &a.mq, h0, first + row0, &sh.q_full[0]);
+    copy(sk, &a.mk, kvh, first, &sh.k_full[0]);
+    if (n1 > 0) copy(sq + kPaTileBytes, &a.mq, h0 + a.pair, first + row1, &sh.q_full[1]);
+    copy(sv, &a.mv, kvh, first, &sh.v_full[0]);
+    if (guard0 == 0) mbar_arrive(&sh.guard_go[0]);
   }
   if (threadIdx.x < 8) sh.odd[threadIdx.x >> 2][threadIdx.x & 3] = 0;
   if (warp == 8) tmem_alloc(&sh.tmem, 512);
@@ -408,24 +422,16 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     } else if (warp == 10) {
       if (elect_one()) {
         bool ok = true;
-        auto tile = [&](unsigned char* dst, const CUtensorMap* map, int h, int tok, uint64_t* bar) {
-          mbar_arrive_expect_tx(bar, kPaTileBytes);
-          tma_load_3d(dst, map, 0, h, tok, bar);
-          tma_load_3d(dst + kPaHalf, map, 64, h, tok, bar);
-        };
-        tile(sq, &a.mq, h0, first + row0, &sh.q_full[0]);
-        int j = 0;
+        int j = 1;  // block 0 is on its way
         for (; j < nb; ++j) {
           const int s = j % kPaStages;
           const uint32_t par = (j / kPaStages + 1) & 1;
           if (j >= kPaStages) ok = pa_wait(&sh.k_empty[s], par, &sh, a);
           if (!ok) break;
-          tile(sk + s * kPaTileBytes, &a.mk, kvh, first + j * kPaTile, &sh.k_full[s]);
-          if (j == 0 && n1 > 0)
-            tile(sq + kPaTileBytes, &a.mq, h0 + a.pair, first + row1, &sh.q_full[1]);
+          copy(sk + s * kPaTileBytes, &a.mk, kvh, first + j * kPaTile, &sh.k_full[s]);
           if (j >= kPaStages) ok = pa_wait(&sh.v_empty[s], par, &sh, a);
           if (!ok) break;
-          tile(sv + s * kPaTileBytes, &a.mv, kvh, first + j * kPaTile, &sh.v_full[s]);
+          copy(sv + s * kPaTileBytes, &a.mv, kvh, first + j * kPaTile, &sh.v_full[s]);
           // from here on the stage's phase is this block's
           if (j >= guard0) mbar_arrive(&sh.guard_go[j - guard0]);
         }

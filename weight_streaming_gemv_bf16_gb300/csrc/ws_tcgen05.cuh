@@ -153,6 +153,10 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void regs_raise() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
