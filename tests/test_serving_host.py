@@ -126,16 +126,31 @@ def test_logprobs_workspace(lib):
 
 def test_binding_refuses_tensors_off_the_current_device_or_misshapen(lib, monkeypatch):
     """The binding looks at shapes, types, strides and devices before the call
-    crosses the ABI."""
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    crosses the ABI.  Tensors on the CPU report device -1: taken as the current
+    one, they reach the checks behind that of the device."""
     bf = torch.bfloat16
     q, kv = torch.zeros(8, 4, 128, dtype=bf), torch.zeros(8, 2, 128, dtype=bf)
     cu, out = torch.zeros(2, dtype=torch.int32), torch.zeros(8, 512, dtype=bf)
+    kc = torch.zeros(2, 2, 10, 80, dtype=torch.uint8)
+    st = torch.zeros(2, dtype=torch.int32)
+    f, n = torch.zeros(2, 512), torch.zeros(2, 256)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     with pytest.raises(ValueError, match="current device"):
         wb.prompt_attention(q, kv, kv, cu, out)
+    with pytest.raises(ValueError, match="current device"):
+        wb.kv_store_q4(kv, kv, kc, kc, st, cu_seqlens=torch.zeros(3, dtype=torch.int32))
+    with pytest.raises(ValueError, match="current device"):
+        wb.kv_load_q4(kc, kc, st, kv, kv)
+    with pytest.raises(ValueError, match="current device"):
+        wb.decode_attention_q4(f, n, n, kc, kc, st, kc, out_f32=f)
+    with pytest.raises(ValueError, match="current device"):
+        wb.token_logprobs(f, kc, entropy=torch.zeros(2))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
     with pytest.raises(ValueError, match="heads must be contiguous"):
         wb.prompt_attention(q.transpose(0, 1), kv, kv, cu, out)
-    with pytest.raises(ValueError, match="disagree"):
+    with pytest.raises(ValueError, match="expected .tokens, heads"):
+        wb.prompt_attention(out, kv, kv, cu, out)
+    with pytest.raises(ValueError, match="disagree in shape"):
         wb.prompt_attention(q, kv[:7], kv, cu, out)
     with pytest.raises(ValueError, match="disagree in type"):
         wb.prompt_attention(q, kv.half(), kv, cu, out)
@@ -143,31 +158,29 @@ def test_binding_refuses_tensors_off_the_current_device_or_misshapen(lib, monkey
         wb.prompt_attention(q, kv, kv, cu, out[:, :256])
     with pytest.raises(ValueError, match="cu_seqlens"):
         wb.prompt_attention(q, kv, kv, cu.long(), out)
-    kc = torch.zeros(2, 2, 10, 80, dtype=torch.uint8)
-    st = torch.zeros(2, dtype=torch.int32)
-    with pytest.raises(ValueError, match="current device"):
-        wb.kv_store_q4(kv, kv, kc, kc, st, cu_seqlens=torch.zeros(3, dtype=torch.int32))
+    with pytest.raises(ValueError, match="lse"):
+        wb.prompt_attention(q, kv, kv, cu, out, lse=torch.zeros(4, 8))
     with pytest.raises(ValueError, match="cu_seqlens"):
         wb.kv_store_q4(kv, kv, kc, kc, st, cu_seqlens=cu)
     with pytest.raises(ValueError, match="v_cache"):
         wb.kv_store_q4(kv, kv, kc, kc[:1], st)
+    with pytest.raises(ValueError, match="disagree"):
+        wb.kv_store_q4(kv, kv.half(), kc, kc, st)
+    with pytest.raises(ValueError, match="k_cache"):
+        wb.kv_store_q4(q, q, kc, kc, st)
     with pytest.raises(ValueError, match="contiguous"):
         wb.kv_load_q4(kc, kc, st, kv[::2], kv[::2])
-    f = torch.zeros(2, 512)
-    n = torch.zeros(2, 256)
     with pytest.raises(ValueError, match="pos"):
         wb.decode_attention_q4(f, n, n, kc, kc, st.long(), kc, out_f32=f)
     with pytest.raises(ValueError, match="k_new"):
         wb.decode_attention_q4(f, f, n, kc, kc, st, kc, out_f32=f)
-    with pytest.raises(ValueError, match="current device"):
-        wb.decode_attention_q4(f, n, n, kc, kc, st, kc, out_f32=f)
+    with pytest.raises(ValueError, match="out_bf16"):
+        wb.decode_attention_q4(f, n, n, kc, kc, st, kc, out_bf16=f)
     with pytest.raises(ValueError, match="contiguous"):
         wb.token_logprobs(f.t(), kc)
     with pytest.raises(ValueError, match="top_logprob"):
         wb.token_logprobs(f, kc, top_idx=torch.zeros(2, 4, dtype=torch.int32),
                           top_logprob=torch.zeros(2, 5))
-    with pytest.raises(ValueError, match="current device"):
-        wb.token_logprobs(f, kc, entropy=torch.zeros(2))
 
 
 @pytest.mark.parametrize("keys", [True, False])

@@ -351,35 +351,50 @@ def decode_attention(q, k_new, v_new, k_cache, v_cache, pos, workspace, out_f32=
                                       B, n_heads, n_kv, d, s_max, wp, wb, _stream(stream)))
 
 
-def _here(*tensors):
-    """Refuse tensors that are not on the current device (the library launches there)."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensor on {t.device}: expected the current device, cuda:{dev}")
-
+# The serving operators check their tensors here: type, shape, strides and that
+# they are on the current device, where the library launches.  Each check hands
+# on the pointer (a step's calls are short enough for the host to matter).
 
 def _need(ok, what: str):
     if not ok:
         raise ValueError(what)
 
 
-def _whole(t, dtype, shape, what: str):
-    """Refuse a tensor that is not contiguous, of this type and shape; None passes."""
-    if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
-        raise ValueError(f"{what}: expected contiguous {dtype} {tuple(shape)}, "
-                         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+def _at(t, dtype, shape, dev: int, what: str):
+    """The address of a contiguous tensor of this type and shape; None passes."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        raise ValueError(f"{what} on {t.device}: expected the current device, cuda:{dev}")
+    raise ValueError(f"{what}: expected contiguous {dtype} {tuple(shape)}, "
+                     f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
 
 
-def _token_heads(t, what: str):
-    """[T, heads, d] with each token's heads contiguous -> (T, heads, d, token stride)."""
-    if t.dim() != 3:
-        raise ValueError(f"{what}: expected [tokens, heads, head_dim], got {tuple(t.shape)}")
-    T, n, d = t.shape
+def _tokens_at(t, dev: int, what: str):
+    """[T, heads, d] with each token's heads contiguous -> (shape, token stride, address)."""
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{what}: expected [tokens, heads, head_dim], got {tuple(shape)}")
+    T, n, d = shape
     st, sh, sd = t.stride()
     if (sd != 1 and d > 1) or (sh != d and n > 1):
         raise ValueError(f"{what}: a token's heads must be contiguous, got strides {t.stride()}")
-    return T, n, d, (st if T > 1 else n * d)
+    if t.get_device() != dev:
+        raise ValueError(f"{what} on {t.device}: expected the current device, cuda:{dev}")
+    return shape, (st if T > 1 else n * d), t.data_ptr()
+
+
+def _stream_on(stream, dev: int):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
+
+
+def _space_at(ws, dev: int):
+    _need(ws.get_device() == dev, f"workspace on {ws.device}: expected the current device")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def prompt_attention(q, k, v, cu_seqlens, out, lse=None, stream=None):
@@ -387,19 +402,22 @@ def prompt_attention(q, k, v, cu_seqlens, out, lse=None, stream=None):
     [T, n_kv, 128] in bf16 or fp16 (token strides free, so columns of one
     fused projection will do), cu_seqlens int32 [n_seqs + 1] on the device,
     out [T, n_heads * 128] of the same type, lse fp32 [T, n_heads] or None."""
-    T, nh, d, qs = _token_heads(q, "q")
-    Tk, nkv, dk, ks = _token_heads(k, "k")
-    Tv, nv, dv, vs = _token_heads(v, "v")
-    _need(Tk == T == Tv and nv == nkv and dk == d == dv, "q, k and v disagree in shape")
-    _need(k.dtype == q.dtype == v.dtype, "q, k and v disagree in type")
-    _whole(out, q.dtype, (T, nh * d), "out")
-    _whole(lse, torch.float32, (T, nh), "lse")
-    _need(cu_seqlens.dim() == 1, "cu_seqlens: expected one dimension")
-    _whole(cu_seqlens, torch.int32, cu_seqlens.shape, "cu_seqlens")
-    _here(q, k, v, cu_seqlens, out, lse)
-    _check(load().ws_prompt_attention(_ptr(q), _ptr(k), _ptr(v), _dtype_code(q), _ptr(cu_seqlens),
-                                      _ptr(out), _ptr(lse), T, cu_seqlens.shape[0] - 1, nh, nkv,
-                                      d, qs, ks, vs, _stream(stream)))
+    dev = torch.cuda.current_device()
+    (T, nh, d), qs, qp = _tokens_at(q, dev, "q")
+    kshape, ks, kp = _tokens_at(k, dev, "k")
+    vshape, vs, vp = _tokens_at(v, dev, "v")
+    nkv = kshape[1]
+    _need(kshape == vshape and kshape[0] == T and kshape[2] == d, "q, k and v disagree in shape")
+    dt = q.dtype
+    _need(k.dtype is dt and v.dtype is dt, "q, k and v disagree in type")
+    n = cu_seqlens.shape[0]
+    _check(load().ws_prompt_attention(
+        qp, kp, vp, _dtype_code(q), _at(cu_seqlens, torch.int32, (n,), dev, "cu_seqlens"),
+        _at(out, dt, (T, nh * d), dev, "out"), _at(lse, torch.float32, (T, nh), dev, "lse"), T,
+        n - 1, nh, nkv, d, qs, ks, vs, _stream_on(stream, dev)))
+
+
+_KV_Q4_ROW = 80  # bytes of a cached row, ws_kv_q4_row_bytes(128)
 
 
 def kv_q4_row_bytes(head_dim=128) -> int:
@@ -412,16 +430,16 @@ def new_kv_cache_q4(n_rows, n_kv_heads, s_max, head_dim=128, device="cuda"):
                        device=device)
 
 
-def _kv_q4_args(T, nkv, k_cache, v_cache, start, cu_seqlens, rows):
-    n_rows, n, s_max, rb = k_cache.shape
-    _need(rb == kv_q4_row_bytes() and n == nkv, "k_cache: expected [rows, n_kv, s_max, 80]")
-    _whole(k_cache, torch.uint8, k_cache.shape, "k_cache")
-    _whole(v_cache, torch.uint8, k_cache.shape, "v_cache")
-    n_seqs = start.shape[0]
-    _whole(start, torch.int32, (n_seqs,), "start")
-    _whole(rows, torch.int32, (n_seqs,), "rows")
-    _whole(cu_seqlens, torch.int32, (n_seqs + 1,), "cu_seqlens")
-    return n_seqs, n_rows, s_max
+def _kv_q4_args(nkv, k_cache, v_cache, start, cu_seqlens, rows, dev):
+    shape = k_cache.shape
+    _need(len(shape) == 4 and shape[3] == _KV_Q4_ROW and shape[1] == nkv,
+          "k_cache: expected [rows, n_kv, s_max, 80]")
+    n = start.shape[0]
+    return (_at(cu_seqlens, torch.int32, (n + 1,), dev, "cu_seqlens"),
+            _at(rows, torch.int32, (n,), dev, "rows"),
+            _at(start, torch.int32, (n,), dev, "start"),
+            _at(k_cache, torch.uint8, shape, dev, "k_cache"),
+            _at(v_cache, torch.uint8, shape, dev, "v_cache"), n, shape[0], shape[2])
 
 
 def kv_store_q4(k, v, k_cache, v_cache, start, cu_seqlens=None, rows=None, stream=None):
@@ -429,27 +447,30 @@ def kv_store_q4(k, v, k_cache, v_cache, start, cu_seqlens=None, rows=None, strea
     [n_rows, n_kv, s_max, 80] from slot start[i] on of cache row rows[i] (i
     without `rows`) for the tokens cu_seqlens[i] .. cu_seqlens[i + 1] - 1
     (token i alone without `cu_seqlens`)."""
-    T, nkv, d, ks = _token_heads(k, "k")
-    Tv, nv, dv, vs = _token_heads(v, "v")
-    _need(Tv == T and nv == nkv and dv == d and v.dtype == k.dtype, "k and v disagree")
-    n_seqs, n_rows, s_max = _kv_q4_args(T, nkv, k_cache, v_cache, start, cu_seqlens, rows)
-    _here(k, v, k_cache, v_cache, start, cu_seqlens, rows)
-    _check(load().ws_kv_store_q4(_ptr(k), _ptr(v), _dtype_code(k), _ptr(cu_seqlens), _ptr(rows),
-                                 _ptr(start), _ptr(k_cache), _ptr(v_cache), T, n_seqs, n_rows,
-                                 nkv, d, s_max, ks, vs, _stream(stream)))
+    dev = torch.cuda.current_device()
+    shape, ks, kp = _tokens_at(k, dev, "k")
+    vshape, vs, vp = _tokens_at(v, dev, "v")
+    _need(vshape == shape and v.dtype is k.dtype, "k and v disagree")
+    T, nkv, d = shape
+    cu, rw, st, kc, vc, n, n_rows, s_max = _kv_q4_args(nkv, k_cache, v_cache, start, cu_seqlens,
+                                                       rows, dev)
+    _check(load().ws_kv_store_q4(kp, vp, _dtype_code(k), cu, rw, st, kc, vc, T, n, n_rows, nkv, d,
+                                 s_max, ks, vs, _stream_on(stream, dev)))
 
 
 def kv_load_q4(k_cache, v_cache, start, k, v, cu_seqlens=None, rows=None, stream=None):
     """The values that cached rows stand for, to k and v [T, n_kv, 128] (fp32,
     bf16 or fp16, contiguous); the other arguments as for kv_store_q4."""
-    T, nkv, d, _ = _token_heads(k, "k")
-    _whole(k, k.dtype, k.shape, "k")
-    _whole(v, k.dtype, k.shape, "v")
-    n_seqs, n_rows, s_max = _kv_q4_args(T, nkv, k_cache, v_cache, start, cu_seqlens, rows)
-    _here(k, v, k_cache, v_cache, start, cu_seqlens, rows)
-    _check(load().ws_kv_load_q4(_ptr(k_cache), _ptr(v_cache), _ptr(cu_seqlens), _ptr(rows),
-                                _ptr(start), _ptr(k), _ptr(v), _dtype_code(k), T, n_seqs, n_rows,
-                                nkv, d, s_max, _stream(stream)))
+    dev = torch.cuda.current_device()
+    shape, dt = k.shape, k.dtype
+    _need(len(shape) == 3, "k: expected [tokens, heads, head_dim]")
+    T, nkv, d = shape
+    kp = _at(k, dt, shape, dev, "k")
+    vp = _at(v, dt, shape, dev, "v")
+    cu, rw, st, kc, vc, n, n_rows, s_max = _kv_q4_args(nkv, k_cache, v_cache, start, cu_seqlens,
+                                                       rows, dev)
+    _check(load().ws_kv_load_q4(kc, vc, cu, rw, st, kp, vp, _dtype_code(k), T, n, n_rows, nkv, d,
+                                s_max, _stream_on(stream, dev)))
 
 
 def attention_q4_workspace_bytes(B, n_heads, n_kv_heads, s_max, head_dim=128) -> int:
@@ -461,23 +482,22 @@ def decode_attention_q4(q, k_new, v_new, k_cache, v_cache, pos, workspace, out_f
     """decode_attention over the 4-bit caches uint8 [B, n_kv, s_max, 80]: q
     [B, n_heads*128] fp32, k_new/v_new [B, n_kv*128] fp32 (quantised into the
     caches at pos), pos int32 [B] on the device (negative: no sequence)."""
-    B, nkv, s_max, rb = k_cache.shape
-    d = 128
-    nh = q.shape[1] // d
-    _need(rb == kv_q4_row_bytes(), "k_cache: expected [B, n_kv, s_max, 80]")
-    _whole(k_cache, torch.uint8, k_cache.shape, "k_cache")
-    _whole(v_cache, torch.uint8, k_cache.shape, "v_cache")
-    _whole(q, torch.float32, (B, nh * d), "q")
-    _whole(k_new, torch.float32, (B, nkv * d), "k_new")
-    _whole(v_new, torch.float32, (B, nkv * d), "v_new")
-    _whole(pos, torch.int32, (B,), "pos")
-    _whole(out_f32, torch.float32, (B, nh * d), "out_f32")
-    _whole(out_bf16, torch.bfloat16, (B, nh * d), "out_bf16")
-    _here(q, k_new, v_new, k_cache, v_cache, pos, workspace, out_f32, out_bf16)
-    wp, wb = _ws(workspace)
-    _check(load().ws_decode_attention_q4(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache),
-                                         _ptr(v_cache), _ptr(pos), _ptr(out_f32), _ptr(out_bf16),
-                                         B, nh, nkv, d, s_max, wp, wb, _stream(stream)))
+    dev = torch.cuda.current_device()
+    shape = k_cache.shape
+    _need(len(shape) == 4 and shape[3] == _KV_Q4_ROW, "k_cache: expected [B, n_kv, s_max, 80]")
+    B, nkv, s_max, _ = shape
+    d, f32 = 128, torch.float32
+    nh = q.shape[-1] // d
+    new = (B, nkv * d)
+    heads = (B, nh * d)
+    wp, wb = _space_at(workspace, dev)
+    _check(load().ws_decode_attention_q4(
+        _at(q, f32, heads, dev, "q"), _at(k_new, f32, new, dev, "k_new"),
+        _at(v_new, f32, new, dev, "v_new"), _at(k_cache, torch.uint8, shape, dev, "k_cache"),
+        _at(v_cache, torch.uint8, shape, dev, "v_cache"),
+        _at(pos, torch.int32, (B,), dev, "pos"), _at(out_f32, f32, heads, dev, "out_f32"),
+        _at(out_bf16, torch.bfloat16, heads, dev, "out_bf16"), B, nh, nkv, d, s_max, wp, wb,
+        _stream_on(stream, dev)))
 
 
 def logprobs_workspace_bytes(rows, V, topk=0) -> int:
@@ -489,21 +509,21 @@ def token_logprobs(logits, workspace, targets=None, logprob=None, entropy=None, 
     """Log-probabilities over logits [rows, V] (fp32, bf16 or fp16; rows may be
     padded): logprob fp32 [rows] of targets int32 [rows], entropy fp32 [rows],
     top_idx int32 and top_logprob fp32 [rows, topk]; each output may be None."""
+    dev = torch.cuda.current_device()
     rows, V = logits.shape
-    _need(logits.stride(1) == 1 or V == 1, "logits: a row's values must be contiguous")
-    ld = logits.stride(0) if rows > 1 else V
+    st, s1 = logits.stride()
+    _need(s1 == 1 or V == 1, "logits: a row's values must be contiguous")
+    _need(logits.get_device() == dev, f"logits on {logits.device}: expected the current device")
     top = top_idx if top_idx is not None else top_logprob
-    topk = 0 if top is None else top.shape[1]
-    _whole(targets, torch.int32, (rows,), "targets")
-    _whole(logprob, torch.float32, (rows,), "logprob")
-    _whole(entropy, torch.float32, (rows,), "entropy")
-    _whole(top_idx, torch.int32, (rows, topk), "top_idx")
-    _whole(top_logprob, torch.float32, (rows, topk), "top_logprob")
-    _here(logits, workspace, targets, logprob, entropy, top_idx, top_logprob)
-    wp, wb = _ws(workspace)
-    _check(load().ws_token_logprobs(_ptr(logits), _dtype_code(logits), ld, _ptr(targets),
-                                    _ptr(logprob), _ptr(entropy), _ptr(top_idx),
-                                    _ptr(top_logprob), rows, V, topk, wp, wb, _stream(stream)))
+    topk = 0 if top is None else top.shape[-1]
+    f32, i32, row, alt = torch.float32, torch.int32, (rows,), (rows, topk)
+    wp, wb = _space_at(workspace, dev)
+    _check(load().ws_token_logprobs(
+        logits.data_ptr(), _dtype_code(logits), st if rows > 1 else V,
+        _at(targets, i32, row, dev, "targets"), _at(logprob, f32, row, dev, "logprob"),
+        _at(entropy, f32, row, dev, "entropy"), _at(top_idx, i32, alt, dev, "top_idx"),
+        _at(top_logprob, f32, alt, dev, "top_logprob"), rows, V, topk, wp, wb,
+        _stream_on(stream, dev)))
 
 
 def rmsnorm(x, gamma, y, eps, stream=None):

@@ -25,6 +25,7 @@
 //               do attend to such a value get its share at the end.
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "ws_kv_q4.cuh"
 #include "ws_tcgen05.cuh"
@@ -264,10 +265,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     float m = -1e30f;
     float2 l = make_float2(0.f, 0.f);
     bool ok = true;
-    for (int j = 0; j < n && ok; ++j) {
+    // one block of keys; the last one holds the diagonal
+    auto softmax = [&](int j, auto diagonal) {
       ok = pa_wait(&sh.s_full[tile], j & 1, &sh, a);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+      if (!ok) return;
       tc_fence_after();
       uint32_t s[128], mx[4];
 #pragma unroll
@@ -275,14 +277,22 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       tmem_wait_ld();
       tmem_loaded<128>(s);
       asm volatile("" : "+r"(mx[0]), "+r"(mx[1]), "+r"(mx[2]), "+r"(mx[3]));
-      if (j == n - 1) {  // the diagonal: keys after the row's token
+      if constexpr (decltype(diagonal)::value) {
+        // the diagonal: of the warp's 32 rows, the 32 keys of its own number
+        // are masked one by one, those after them all
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
+          if (c < (warp & 3)) continue;
           float y = -INFINITY;
+          if (c == (warp & 3)) {
 #pragma unroll
-          for (int i = 32 * c; i < 32 * c + 32; ++i) {
-            if (i > r) s[i] = 0xff800000u;
-            y = fmaxf(y, __uint_as_float(s[i]));
+            for (int i = 0; i < 32; ++i) {
+              if (i > lane) s[32 * c + i] = 0xff800000u;
+              y = fmaxf(y, __uint_as_float(s[32 * c + i]));
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[32 * c + i] = 0xff800000u;
           }
           mx[c] = __float_as_uint(y);
         }
@@ -326,7 +336,10 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p_full[tile][h]);
       }
-    }
+    };
+#pragma unroll 1
+    for (int j = 0; j < n - 1 && ok; ++j) softmax(j, std::false_type());
+    if (n > 0 && ok) softmax(n - 1, std::true_type());
     if (n > 0 && ok) ok = __all_sync(0xffffffffu, pa_wait(&sh.o_full[tile], 0, &sh, a));
     if (n > 0 && ok) {
       tc_fence_after();
