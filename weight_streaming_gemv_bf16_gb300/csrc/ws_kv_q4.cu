@@ -3,8 +3,8 @@
 // fp16; and the cached rows back as the values they stand for.
 //
 // Bound by DRAM: a token and key-value head reads 512 bytes (16-bit) and
-// writes 160.  A warp takes one token and head, lanes 0..15 its key row and
-// 16..31 its value row, eight dimensions a lane, so that a group of 32 is a
+// writes 160.  A warp takes a token and head at a time, lanes 0..15 its key row
+// and 16..31 its value row, eight dimensions a lane, so that a group of 32 is a
 // quad: its minimum and maximum are two shuffles away and nothing passes
 // through shared memory.  A CTA's warps take consecutive tokens of one head:
 // their rows are neighbours in the cache.
@@ -26,75 +26,122 @@ struct KvRowsParams {
   unsigned char* vc;
   long long ks, vs;
   int T, n, n_rows, nkv, S;
+  int per;  // tokens a warp
   int* err;
+};
+
+// Where tokens go: the sequence that the last token asked for was in.
+struct KvPlace {
+  int lo, hi;  // its tokens
+  int row, s0;  // cache row, slot of token lo (negative: none)
 };
 
 // Cache row and slot of token t; false where it has none.  bad: a row or slot
 // outside the cache (no access is made there).
-__device__ __forceinline__ bool kv_place(const KvRowsParams& a, int t, int& row, int& slot,
+__device__ __forceinline__ bool kv_place(const KvRowsParams& a, int t, KvPlace& p, int& slot,
                                          bool& bad) {
-  int i = t, off = 0;
   bad = false;
-  if (a.cu) {
-    int lo = 0, hi = a.n;  // the last bound at or before t
-    if (a.cu[0] > t) return false;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (a.cu[mid] <= t) lo = mid; else hi = mid - 1;
+  if (t < p.lo || t >= p.hi) {
+    int i = t;
+    p.lo = t;
+    p.hi = t + 1;
+    if (a.cu) {
+      int lo = 0, hi = a.n;  // the last bound at or before t
+      p.s0 = -1;
+      if (a.cu[0] > t) return false;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.cu[mid] <= t) lo = mid; else hi = mid - 1;
+      }
+      if (lo >= a.n || a.cu[lo + 1] <= t) return false;
+      i = lo;
+      p.lo = a.cu[lo];
+      p.hi = a.cu[lo + 1];
     }
-    if (lo >= a.n || a.cu[lo + 1] <= t) return false;
-    i = lo;
-    off = t - a.cu[lo];
+    p.s0 = a.start[i];
+    p.row = a.rows ? a.rows[i] : i;
   }
-  const int s0 = a.start[i];
-  if (s0 < 0) return false;
-  row = a.rows ? a.rows[i] : i;
-  bad = row < 0 || row >= a.n_rows || s0 >= a.S || off >= a.S - s0;
-  slot = s0 + off;
+  if (p.s0 < 0) return false;
+  const int off = t - p.lo;
+  bad = p.row < 0 || p.row >= a.n_rows || p.s0 >= a.S || off >= a.S - p.s0;
+  slot = p.s0 + off;
   return !bad;
 }
 
+constexpr int kKvWarps = 8;
+constexpr int kKvBatch = 4;  // tokens whose loads a warp has in flight together
+
+// A warp takes `per` tokens of one head, kKvWarps apart.
 template <int DT>
-__global__ void __launch_bounds__(256) k_kv_store_q4(const __grid_constant__ KvRowsParams a) {
-  const int t = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, g = blockIdx.y;
-  if (t >= a.T) return;
-  int row, slot;
-  bool bad;
-  if (!kv_place(a, t, row, slot, bad)) {
-    if (bad && lane == 0) atomicExch(a.err, kDerrBadSlot);
-    return;
-  }
+__global__ void __launch_bounds__(kKvWarps * 32, 4) k_kv_store_q4(const __grid_constant__ KvRowsParams a) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = blockIdx.y;
+  const int base = blockIdx.x * kKvWarps * a.per + warp;
   const bool keys = lane < 16;
-  const size_t es = DT == DT_F32 ? 4 : 2;
-  const char* src = static_cast<const char*>(keys ? a.k : a.v) +
-                    ((size_t)t * (keys ? a.ks : a.vs) + (size_t)g * kKvDim + (lane & 15) * 8) * es;
-  float x[8];
-  load8<DT>(src, x);
-  uint32_t sz;
-  const uint32_t w = quantize8(x, sz);
-  unsigned char* dst = (keys ? a.kc : a.vc) + (((size_t)row * a.nkv + g) * a.S + slot) * kKvRow;
-  put_row(dst, w, sz, keys, true);
+  constexpr size_t es = DT == DT_F32 ? 4 : 2;
+  const char* src = static_cast<const char*>(keys ? a.k : a.v) + ((size_t)g * kKvDim + (lane & 15) * 8) * es;
+  const size_t stride = (size_t)(keys ? a.ks : a.vs) * es;
+  unsigned char* cache = keys ? a.kc : a.vc;
+  KvPlace place = {0, 0, 0, -1};
+  for (int i = 0; i < a.per; i += kKvBatch) {
+    uint4 raw[kKvBatch][DT == DT_F32 ? 2 : 1];
+    unsigned char* dst[kKvBatch];
+#pragma unroll
+    for (int u = 0; u < kKvBatch; ++u) {
+      const int t = base + (i + u) * kKvWarps;
+      int slot;
+      bool bad = false;
+      dst[u] = nullptr;
+      if (i + u < a.per && t < a.T) {
+#pragma unroll
+        for (int e = 0; e < (DT == DT_F32 ? 2 : 1); ++e)
+          raw[u][e] = __ldcs(reinterpret_cast<const uint4*>(src + t * stride) + e);
+        if (kv_place(a, t, place, slot, bad))
+          dst[u] = cache + (((size_t)place.row * a.nkv + g) * a.S + slot) * kKvRow;
+        if (bad && lane == 0) atomicExch(a.err, kDerrBadSlot);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kKvBatch; ++u) {
+      if (!dst[u]) continue;  // alike in the whole warp
+      float x[8];
+      load8<DT>(raw[u], x);
+      uint32_t sz;
+      const uint32_t w = quantize8(x, sz);
+      put_row(dst[u], w, sz, keys, true);
+    }
+  }
 }
 
 template <int DT>
-__global__ void __launch_bounds__(256) k_kv_load_q4(const __grid_constant__ KvRowsParams a) {
-  const int t = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31, g = blockIdx.y;
-  if (t >= a.T) return;
-  int row, slot;
-  bool bad;
-  if (!kv_place(a, t, row, slot, bad)) {
-    if (bad && lane == 0) atomicExch(a.err, kDerrBadSlot);
-    return;
-  }
+__global__ void __launch_bounds__(kKvWarps * 32) k_kv_load_q4(const __grid_constant__ KvRowsParams a) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = blockIdx.y;
+  const int base = blockIdx.x * kKvWarps * a.per + warp;
   const bool keys = lane < 16;
-  const size_t es = DT == DT_F32 ? 4 : 2;
-  const unsigned char* src =
-      (keys ? a.kc : a.vc) + (((size_t)row * a.nkv + g) * a.S + slot) * kKvRow;
-  float x[8];
-  get_row(src, keys, x);
-  char* dst = static_cast<char*>(keys ? a.k_out : a.v_out) +
-              (((size_t)t * a.nkv + g) * kKvDim + (lane & 15) * 8) * es;
-  store8<DT>(dst, x);
+  constexpr size_t es = DT == DT_F32 ? 4 : 2;
+  const unsigned char* cache = keys ? a.kc : a.vc;
+  char* out = static_cast<char*>(keys ? a.k_out : a.v_out) + ((size_t)g * kKvDim + (lane & 15) * 8) * es;
+  KvPlace place = {0, 0, 0, -1};
+  for (int i = 0; i < a.per; i += kKvBatch) {
+    KvWord word[kKvBatch];
+    bool there[kKvBatch];
+#pragma unroll
+    for (int u = 0; u < kKvBatch; ++u) {
+      const int t = base + (i + u) * kKvWarps;
+      int slot;
+      bool bad = false;
+      there[u] = i + u < a.per && t < a.T && kv_place(a, t, place, slot, bad);
+      if (there[u])
+        word[u] = get_word(cache + (((size_t)place.row * a.nkv + g) * a.S + slot) * kKvRow, keys);
+      if (bad && lane == 0) atomicExch(a.err, kDerrBadSlot);
+    }
+#pragma unroll
+    for (int u = 0; u < kKvBatch; ++u) {
+      if (!there[u]) continue;
+      float x[8];
+      word_values(word[u], x);
+      store8<DT>(out + (size_t)(base + (i + u) * kKvWarps) * a.nkv * kKvDim * es, x);
+    }
+  }
 }
 
 static bool misaligned(const void* p) { return ((uintptr_t)p & 15u) != 0; }
@@ -129,15 +176,18 @@ static ws_status kv_rows(KvRowsParams& a, int dtype, int head_dim, bool store,
     set_error("device error flag unavailable");
     return WS_ERR_CUDA;
   }
-  const dim3 grid((a.T + 7) / 8, a.nkv);
+  // few rows: a warp each, for the shortest time; many: 8 a warp, so that the
+  // search for a token's sequence is made once and four loads are in flight
+  a.per = (long long)a.T * a.nkv > 16 * 1024 ? 8 : 1;
+  const dim3 grid((a.T + kKvWarps * a.per - 1) / (kKvWarps * a.per), a.nkv);
   if (store) {
-    if (dtype == WS_DTYPE_F32) k_kv_store_q4<DT_F32><<<grid, 256, 0, stream>>>(a);
-    else if (dtype == WS_DTYPE_BF16) k_kv_store_q4<DT_BF16><<<grid, 256, 0, stream>>>(a);
-    else k_kv_store_q4<DT_F16><<<grid, 256, 0, stream>>>(a);
+    if (dtype == WS_DTYPE_F32) k_kv_store_q4<DT_F32><<<grid, kKvWarps * 32, 0, stream>>>(a);
+    else if (dtype == WS_DTYPE_BF16) k_kv_store_q4<DT_BF16><<<grid, kKvWarps * 32, 0, stream>>>(a);
+    else k_kv_store_q4<DT_F16><<<grid, kKvWarps * 32, 0, stream>>>(a);
   } else {
-    if (dtype == WS_DTYPE_F32) k_kv_load_q4<DT_F32><<<grid, 256, 0, stream>>>(a);
-    else if (dtype == WS_DTYPE_BF16) k_kv_load_q4<DT_BF16><<<grid, 256, 0, stream>>>(a);
-    else k_kv_load_q4<DT_F16><<<grid, 256, 0, stream>>>(a);
+    if (dtype == WS_DTYPE_F32) k_kv_load_q4<DT_F32><<<grid, kKvWarps * 32, 0, stream>>>(a);
+    else if (dtype == WS_DTYPE_BF16) k_kv_load_q4<DT_BF16><<<grid, kKvWarps * 32, 0, stream>>>(a);
+    else k_kv_load_q4<DT_F16><<<grid, kKvWarps * 32, 0, stream>>>(a);
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {

@@ -101,12 +101,35 @@ __device__ __forceinline__ uint32_t quantize8(const float (&x)[8], uint32_t& sz)
   const float z = __bfloat162float(__float2bfloat16_rn(__fadd_rn(lo, 8.f * s)));
   sz = (__float_as_uint(s) >> 16) | (__float_as_uint(z) & 0xffff0000u);
   if (s == 0.f) return 0x88888888u;
-  uint32_t w = 0;
+  // n = rint(d / s), d = x - z: rounded from the product with an approximate
+  // 1 / s, then held against the exact remainder d - n s (n s has 12 bits), which
+  // is at most s / 2, and s / 2 only for an even n.  (The rounded quotient is a
+  // tie only where d / s is one: d next to (n + 1/2) s is at least 2^-24 of it
+  // away, more than half a unit of n + 1/2.)  Adding 1.5 2^23 + 8 rounds to even
+  // and leaves n + 8 in the low bits.
+  constexpr float kMagic = 12582912.f;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  const float half = 0.5f * s;
+  float c[8], rem[8];
+  bool near = false;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float q = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[i], z), s)) + 8.f, 0.f), 15.f);
-    w |= (uint32_t)q << (4 * i);
+    const float d = __fsub_rn(x[i], z);
+    c[i] = __fmaf_rn(d, r, kMagic + 8.f);
+    rem[i] = __fmaf_rn(__fsub_rn(kMagic + 8.f, c[i]), s, d);
+    near |= fabsf(rem[i]) >= half;
   }
+  if (near) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (fabsf(rem[i]) > half || (fabsf(rem[i]) == half && (__float_as_uint(c[i]) & 1u)))
+        c[i] += copysignf(1.f, rem[i]);
+  }
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    w |= (__float_as_uint(fminf(fmaxf(c[i], kMagic), kMagic + 15.f)) & 15u) << (4 * i);
   return w;
 }
 
@@ -134,21 +157,33 @@ __device__ __forceinline__ void put_row(unsigned char* row, uint32_t w, uint32_t
   if (t == 0) reinterpret_cast<uint32_t*>(row + kKvCodes)[g] = sz;
 }
 
-// The eight values that lane l of a row's 16 lanes stores and reads.
-__device__ __forceinline__ void get_row(const unsigned char* row, bool keys, float (&x)[8]) {
+// What lane l of a row's 16 lanes reads: its eight codes and their (s, z); and
+// the values they stand for.
+struct KvWord {
+  uint32_t w, sz;
+};
+__device__ __forceinline__ KvWord get_word(const unsigned char* row, bool keys) {
   const int l = threadIdx.x & 15, g = l >> 2, t = l & 3;
-  uint32_t w;
+  KvWord r;
   if (keys) {
-    w = reinterpret_cast<const uint32_t*>(row)[4 * t + g];
+    r.w = reinterpret_cast<const uint32_t*>(row)[4 * t + g];
   } else {
     const uint16_t* u = reinterpret_cast<const uint16_t*>(row);
-    w = u[4 * (2 * t) + g] | ((uint32_t)u[4 * (2 * t + 1) + g] << 16);
+    r.w = u[4 * (2 * t) + g] | ((uint32_t)u[4 * (2 * t + 1) + g] << 16);
   }
-  const uint32_t sz = reinterpret_cast<const uint32_t*>(row + kKvCodes)[g];
-  const float s = bf16lo(sz), z = bf16hi(sz);
+  r.sz = reinterpret_cast<const uint32_t*>(row + kKvCodes)[g];
+  return r;
+}
+__device__ __forceinline__ void word_values(const KvWord& r, float (&x)[8]) {
+  const float s = bf16lo(r.sz), z = bf16hi(r.sz);
+  const uint32_t even = r.w & 0x0f0f0f0fu, odd = (r.w >> 4) & 0x0f0f0f0fu;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    x[i] = __fadd_rn(__fmul_rn(s, (float)((int)((w >> (4 * i)) & 15u) - 8)), z);
+  for (int i = 0; i < 8; ++i) {
+    // 2^23 + code, a byte into the mantissa; s (code - 8) is exact, so the fma
+    // rounds where the sum does
+    const float c = __uint_as_float(__byte_perm(i & 1 ? odd : even, 0x4b000000u, 0x7540 | (i >> 1)));
+    x[i] = __fmaf_rn(s, __fsub_rn(c, 8388616.f), z);
+  }
 }
 
 template <int DT>
