@@ -30,42 +30,38 @@ struct KvRowsParams {
   int* err;
 };
 
-// Where tokens go: the sequence that the last token asked for was in.
+// Where the tokens of one sequence go, in one head's cache rows.
 struct KvPlace {
-  int lo, hi;  // its tokens
-  int row, s0;  // cache row, slot of token lo (negative: none)
+  int lo, hi;     // its tokens
+  int lim;        // those before lim have a slot
+  bool over;      // those from lim on lack one that they should have
+  size_t at;      // row (of 80 bytes) of token lo
 };
 
-// Cache row and slot of token t; false where it has none.  bad: a row or slot
-// outside the cache (no access is made there).
-__device__ __forceinline__ bool kv_place(const KvRowsParams& a, int t, KvPlace& p, int& slot,
-                                         bool& bad) {
-  bad = false;
-  if (t < p.lo || t >= p.hi) {
-    int i = t;
-    p.lo = t;
-    p.hi = t + 1;
-    if (a.cu) {
-      int lo = 0, hi = a.n;  // the last bound at or before t
-      p.s0 = -1;
-      if (a.cu[0] > t) return false;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.cu[mid] <= t) lo = mid; else hi = mid - 1;
-      }
-      if (lo >= a.n || a.cu[lo + 1] <= t) return false;
-      i = lo;
-      p.lo = a.cu[lo];
-      p.hi = a.cu[lo + 1];
+// The place of the sequence that token t is in (t alone where it is in none).
+// No access is made outside the cache: a row or slot there only sets `over`.
+__device__ __forceinline__ void kv_find(const KvRowsParams& a, int t, int g, KvPlace& p) {
+  int i = t;
+  p = {t, t + 1, t, false, 0};
+  if (a.cu) {
+    int lo = 0, hi = a.n;  // the last bound at or before t
+    if (a.cu[0] > t) return;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.cu[mid] <= t) lo = mid; else hi = mid - 1;
     }
-    p.s0 = a.start[i];
-    p.row = a.rows ? a.rows[i] : i;
+    if (lo >= a.n || a.cu[lo + 1] <= t) return;
+    i = lo;
+    p.lo = p.lim = a.cu[lo];
+    p.hi = a.cu[lo + 1];
   }
-  if (p.s0 < 0) return false;
-  const int off = t - p.lo;
-  bad = p.row < 0 || p.row >= a.n_rows || p.s0 >= a.S || off >= a.S - p.s0;
-  slot = p.s0 + off;
-  return !bad;
+  const int s0 = a.start[i], row = a.rows ? a.rows[i] : i;
+  if (s0 < 0) return;
+  if (row >= 0 && row < a.n_rows && s0 < a.S) {
+    p.lim = p.lo + min(p.hi - p.lo, a.S - s0);
+    p.at = ((size_t)row * a.nkv + g) * a.S + s0;
+  }
+  p.over = p.lim < p.hi;
 }
 
 constexpr int kKvWarps = 8;
@@ -81,23 +77,21 @@ __global__ void __launch_bounds__(kKvWarps * 32, 4) k_kv_store_q4(const __grid_c
   const char* src = static_cast<const char*>(keys ? a.k : a.v) + ((size_t)g * kKvDim + (lane & 15) * 8) * es;
   const size_t stride = (size_t)(keys ? a.ks : a.vs) * es;
   unsigned char* cache = keys ? a.kc : a.vc;
-  KvPlace place = {0, 0, 0, -1};
+  KvPlace place = {0, 0, 0, false, 0};
   for (int i = 0; i < a.per; i += kKvBatch) {
     uint4 raw[kKvBatch][DT == DT_F32 ? 2 : 1];
     unsigned char* dst[kKvBatch];
 #pragma unroll
     for (int u = 0; u < kKvBatch; ++u) {
       const int t = base + (i + u) * kKvWarps;
-      int slot;
-      bool bad = false;
       dst[u] = nullptr;
       if (i + u < a.per && t < a.T) {
 #pragma unroll
         for (int e = 0; e < (DT == DT_F32 ? 2 : 1); ++e)
           raw[u][e] = __ldcs(reinterpret_cast<const uint4*>(src + t * stride) + e);
-        if (kv_place(a, t, place, slot, bad))
-          dst[u] = cache + (((size_t)place.row * a.nkv + g) * a.S + slot) * kKvRow;
-        if (bad && lane == 0) atomicExch(a.err, kDerrBadSlot);
+        if (t < place.lo || t >= place.hi) kv_find(a, t, g, place);
+        if (t < place.lim) dst[u] = cache + (place.at + (t - place.lo)) * kKvRow;
+        else if (place.over && lane == 0) atomicExch(a.err, kDerrBadSlot);
       }
     }
 #pragma unroll
@@ -120,19 +114,19 @@ __global__ void __launch_bounds__(kKvWarps * 32) k_kv_load_q4(const __grid_const
   constexpr size_t es = DT == DT_F32 ? 4 : 2;
   const unsigned char* cache = keys ? a.kc : a.vc;
   char* out = static_cast<char*>(keys ? a.k_out : a.v_out) + ((size_t)g * kKvDim + (lane & 15) * 8) * es;
-  KvPlace place = {0, 0, 0, -1};
+  KvPlace place = {0, 0, 0, false, 0};
   for (int i = 0; i < a.per; i += kKvBatch) {
     KvWord word[kKvBatch];
     bool there[kKvBatch];
 #pragma unroll
     for (int u = 0; u < kKvBatch; ++u) {
       const int t = base + (i + u) * kKvWarps;
-      int slot;
-      bool bad = false;
-      there[u] = i + u < a.per && t < a.T && kv_place(a, t, place, slot, bad);
-      if (there[u])
-        word[u] = get_word(cache + (((size_t)place.row * a.nkv + g) * a.S + slot) * kKvRow, keys);
-      if (bad && lane == 0) atomicExch(a.err, kDerrBadSlot);
+      there[u] = i + u < a.per && t < a.T;
+      if (!there[u]) continue;
+      if (t < place.lo || t >= place.hi) kv_find(a, t, g, place);
+      there[u] = t < place.lim;
+      if (there[u]) word[u] = get_word(cache + (place.at + (t - place.lo)) * kKvRow, keys);
+      else if (place.over && lane == 0) atomicExch(a.err, kDerrBadSlot);
     }
 #pragma unroll
     for (int u = 0; u < kKvBatch; ++u) {

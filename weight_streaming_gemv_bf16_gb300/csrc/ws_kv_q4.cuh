@@ -44,6 +44,16 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -80,12 +90,10 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 // 8 s); q = clamp(rint((x - z) / s) + 8, 0, 15), 8 where s is 0.  A group
 // with a value that is not finite stands for NaN as a whole.
 __device__ __forceinline__ uint32_t quantize8(const float (&x)[8], uint32_t& sz) {
-  float lo = x[0], hi = x[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    lo = min_nan(lo, x[i]);
-    hi = max_nan(hi, x[i]);
-  }
+  float lo = min_nan(min3_nan(x[0], x[1], x[2]), min3_nan(x[3], x[4], x[5]));
+  float hi = max_nan(max3_nan(x[0], x[1], x[2]), max3_nan(x[3], x[4], x[5]));
+  lo = min3_nan(lo, x[6], x[7]);
+  hi = max3_nan(hi, x[6], x[7]);
 #pragma unroll
   for (int o = 1; o <= 2; o <<= 1) {
     lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
@@ -126,10 +134,12 @@ __device__ __forceinline__ uint32_t quantize8(const float (&x)[8], uint32_t& sz)
       if (fabsf(rem[i]) > half || (fabsf(rem[i]) == half && (__float_as_uint(c[i]) & 1u)))
         c[i] += copysignf(1.f, rem[i]);
   }
+  // two codes at a time, clamped to 4 bits, above the ones before them
   uint32_t w = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    w |= (__float_as_uint(fminf(fmaxf(c[i], kMagic), kMagic + 15.f)) & 15u) << (4 * i);
+  for (int i = 6; i >= 0; i -= 2)
+    asm("cvt.pack.sat.u4.s32.b32 %0, %1, %2, %0;"
+        : "+r"(w) : "r"(__float_as_int(c[i + 1]) - 0x4b400000), "r"(__float_as_int(c[i]) - 0x4b400000));
   return w;
 }
 
