@@ -4,6 +4,8 @@
 // With m = max x, Z = sum e^(x - m): log p_i = x_i - m - log Z, and the
 // entropy -sum p log p = log Z - sum e^(x - m) (x - m) / Z.
 #include <cmath>
+#include <cstddef>
+#include <mutex>
 
 #include "ws_kv_q4.cuh"
 
@@ -12,14 +14,14 @@
 namespace ws {
 
 constexpr int kMaxTop = 32;         // alternatives a row: one a lane
-constexpr int kLpThreads = 256;
+constexpr int kLpThreads = 128;
 constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kLpEach = 16;         // values a thread takes at once
-constexpr int kLpStep = kLpThreads * kLpEach;
+constexpr int kLpBytes = 64;        // of values that a thread takes at once
+constexpr int kLpStep = kLpThreads * kLpBytes / 2;  // values a step at most
+constexpr int kLpStages = 2;        // steps on their way or worked on
 constexpr int kLpCompact = 64;      // candidates that make the CTA sort out the best ones
-constexpr int kLpBuf = kLpCompact + kLpStep + 2 * kLpEach;
-static_assert(kLpBuf >= 64 * kMaxTop, "the splits' best fit");
-constexpr int kLpSplits = 64;       // CTAs a row at most
+constexpr int kLpBuf = 512;         // candidates there is room for
+constexpr int kLpSplits = 48;       // CTAs a row at most
 constexpr int kLpCtas = 608;        // CTAs that a small batch's rows are cut into
 constexpr float kLpFar = -1e4f;     // e^y is 0 long before: stands for -infinity in sums
 constexpr float kLog2e = 1.4426950408889634f;
@@ -38,6 +40,7 @@ struct LogprobParams {
   float4* stat;                // [rows][splits]: max, sum, sum e y
   unsigned long long* keys;    // [rows][splits][k]
   int* err;
+  unsigned long long timeout_ns;
 };
 
 // A key that orders as (value, lower index): the value's bits made monotone,
@@ -104,47 +107,75 @@ struct LpSum {
   }
 };
 
-// 16 values in registers as they came; the largest; x - m of each; each value
+// 64 bytes of values in registers as they came
 template <int DT>
 struct LpRegs {
   static constexpr int kVec = DT == DT_F32 ? 4 : 8;  // values a 16-byte load
-  uint4 u[kLpEach / kVec];
+  static constexpr int kEach = kLpBytes / 16 * kVec;
+  uint4 u[kLpBytes / 16];
+  __device__ __forceinline__ uint32_t word(int i) const {
+    return reinterpret_cast<const uint32_t*>(u)[i];
+  }
   __device__ __forceinline__ float value(int i) const {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
-    if constexpr (DT == DT_F32) return __uint_as_float(w[i]);
-    const uint32_t h = w[i >> 1];
+    if constexpr (DT == DT_F32) return __uint_as_float(word(i));
+    const uint32_t h = word(i >> 1);
     if constexpr (DT == DT_F16) {
       const __half2 v = *reinterpret_cast<const __half2*>(&h);
       return i & 1 ? __high2float(v) : __low2float(v);
     }
     return i & 1 ? bf16hi(h) : bf16lo(h);
   }
-  __device__ __forceinline__ float largest() const {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
+  __device__ __forceinline__ float largest() const {  // NaN only where nothing else is there
     if constexpr (DT == DT_F32) {
       float m = value(0);
 #pragma unroll
-      for (int i = 1; i < kLpEach; ++i) m = fmaxf(m, value(i));
+      for (int i = 1; i < kEach; ++i) m = fmaxf(m, value(i));
       return m;
     } else if constexpr (DT == DT_BF16) {
-      __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&w[0]);
+      __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&u[0].x);
 #pragma unroll
-      for (int i = 1; i < kLpEach / 2; ++i)
-        m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+      for (int i = 1; i < kEach / 2; ++i) {
+        const uint32_t w = word(i);
+        m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&w));
+      }
       return fmaxf(__low2float(m), __high2float(m));
     } else {
-      __half2 m = *reinterpret_cast<const __half2*>(&w[0]);
+      __half2 m = *reinterpret_cast<const __half2*>(&u[0].x);
 #pragma unroll
-      for (int i = 1; i < kLpEach / 2; ++i) m = __hmax2(m, *reinterpret_cast<const __half2*>(&w[i]));
+      for (int i = 1; i < kEach / 2; ++i) {
+        const uint32_t w = word(i);
+        m = __hmax2(m, *reinterpret_cast<const __half2*>(&w));
+      }
       return fmaxf(__low2float(m), __high2float(m));
     }
+  }
+  // whether value 2 i or 2 i + 1 is at least thr (`packed`: thr rounded down, twice)
+  __device__ __forceinline__ bool pair_reaches(int i, float thr, uint32_t packed) const {
+    if constexpr (DT == DT_F32) {
+      return fmaxf(value(2 * i), value(2 * i + 1)) >= thr;
+    } else {
+      const uint32_t w = word(i);
+      if constexpr (DT == DT_BF16)
+        return __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w),
+                           *reinterpret_cast<const __nv_bfloat162*>(&packed)) != 0;
+      else
+        return __hge2_mask(*reinterpret_cast<const __half2*>(&w),
+                           *reinterpret_cast<const __half2*>(&packed)) != 0;
+    }
+  }
+  static __device__ __forceinline__ uint32_t pack_down(float thr) {
+    if constexpr (DT == DT_F32) return 0;
+    uint32_t h;
+    if constexpr (DT == DT_BF16) h = __bfloat16_as_ushort(__float2bfloat16_rd(thr));
+    else h = __half_as_ushort(__float2half_rd(thr));
+    return h | (h << 16);
   }
   // x - m, one rounding: for the 16-bit types by the mixed fma 1 x + (-m)
   __device__ __forceinline__ float diff(int i, float neg_m) const {
     if constexpr (DT == DT_F32) {
       return value(i) + neg_m;
     } else {
-      const uint32_t h = reinterpret_cast<const uint32_t*>(u)[i >> 1];
+      const uint32_t h = word(i >> 1);
       float r;
       if constexpr (DT == DT_BF16) {
         if (i & 1)
@@ -166,12 +197,22 @@ struct LpRegs {
   }
 };
 
+template <int DT>
+__device__ __forceinline__ float lp_value(const void* row, int i) {
+  if constexpr (DT == DT_F32) return static_cast<const float*>(row)[i];
+  const uint16_t u = static_cast<const uint16_t*>(row)[i];
+  if constexpr (DT == DT_F16) return __half2float(__ushort_as_half(u));
+  return __uint_as_float((uint32_t)u << 16);
+}
+
 // The lanes' keys in falling order; then merged with a list in falling order.
-__device__ __forceinline__ unsigned long long lp_exchange(unsigned long long k, int o, bool keep_max) {
-  const unsigned long long p = __shfl_xor_sync(0xffffffffu, k, o);
+template <typename K>
+__device__ __forceinline__ K lp_exchange(K k, int o, bool keep_max) {
+  const K p = __shfl_xor_sync(0xffffffffu, k, o);
   return (p > k) == keep_max ? p : k;
 }
-__device__ __forceinline__ unsigned long long lp_sort(unsigned long long k, int lane) {
+template <typename K>
+__device__ __forceinline__ K lp_sort(K k, int lane) {
 #pragma unroll
   for (int n = 2; n <= 32; n <<= 1)
 #pragma unroll
@@ -179,9 +220,9 @@ __device__ __forceinline__ unsigned long long lp_sort(unsigned long long k, int 
       k = lp_exchange(k, o, ((lane & o) == 0) == ((lane & n) == 0 || n == 32));
   return k;
 }
-__device__ __forceinline__ unsigned long long lp_merge(unsigned long long a, unsigned long long b,
-                                                       int lane) {
-  const unsigned long long r = __shfl_sync(0xffffffffu, b, 31 - lane);
+template <typename K>
+__device__ __forceinline__ K lp_merge(K a, K b, int lane) {
+  const K r = __shfl_sync(0xffffffffu, b, 31 - lane);
   a = a > r ? a : r;  // the 32 largest of both, rising then falling
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) a = lp_exchange(a, o, (lane & o) == 0);
@@ -189,21 +230,25 @@ __device__ __forceinline__ unsigned long long lp_merge(unsigned long long a, uns
 }
 
 struct LpShared {
-  unsigned long long buf[kLpBuf];
-  unsigned long long list[kLpWarps][32];
+  uint64_t full[kLpStages];
   unsigned long long thr;   // a candidate's key is at least this
-  int n;                    // candidates
   LpSum sums[kLpWarps];
-  int last;
+  int n;                    // candidates
+  int last, abort;
+  unsigned long long list[kLpWarps][32];
+  unsigned long long buf[kLpBuf];  // (not there without alternatives)
 };
+constexpr int kLpRing = kLpStages * kLpThreads * kLpBytes;
+static_assert(kLpRing >= kLpSplits * kMaxTop * 8, "the ring takes the splits' best");
 
-// The whole CTA: the 32 largest of the candidates, in falling order, become
-// the only ones.  bar: the threshold becomes the k-th of them, plus `plus`.
-__device__ __forceinline__ void lp_compact(LpShared& sh, int n, int k, int plus) {
+// The whole CTA: the 32 largest of the n keys at `from`, in falling order,
+// become the only candidates, and the threshold the k-th of them plus `plus`.
+__device__ __noinline__ void lp_compact(LpShared& sh, const unsigned long long* from, int n, int k,
+                                        int plus) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   unsigned long long mine = 0;
   for (int i = warp * 32; i < n; i += kLpThreads) {
-    const unsigned long long key = i + lane < n ? sh.buf[i + lane] : 0;
+    const unsigned long long key = i + lane < n ? from[i + lane] : 0;
     if (__any_sync(0xffffffffu, key > __shfl_sync(0xffffffffu, mine, k - 1)))
       mine = lp_merge(mine, lp_sort(key, lane), lane);
   }
@@ -225,17 +270,17 @@ __device__ __forceinline__ void lp_compact(LpShared& sh, int n, int k, int plus)
   __syncthreads();
 }
 
-// One CTA per (split, row).  DRAM bound: 64 bytes (32 of the 16-bit types) a
-// thread are in flight while the last ones are worked on, one barrier for
-// every 4096 values.  The best `k` are found in the same pass: the k-th of the
-// threads' best values of the first step bounds the k-th of all from below, so
-// that only the few values from there on become candidates; their best ones
-// raise the bound when there are many, which an order that keeps rising makes
-// slower but not wrong.
+// One CTA per (split, row).  DRAM bound: a ring of four steps of 8 KB in shared
+// memory, filled by bulk copies, three of them under way while one is worked
+// on; registers hold one step only.  The best `k` are found in the same pass:
+// the k-th of the threads' largest values of the first step bounds the k-th of
+// all from below, so that only the few values from there on become candidates;
+// their best ones raise the bound when there are many, which an order that
+// keeps rising makes slower but not wrong.
 template <int DT, bool TOP>
-__global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(const __grid_constant__ LogprobParams a) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  LpShared& sh = *reinterpret_cast<LpShared*>(smem);
+__global__ void __launch_bounds__(kLpThreads, 8) k_token_logprobs(const __grid_constant__ LogprobParams a) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  LpShared& sh = *reinterpret_cast<LpShared*>(smem + kLpRing);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int r = blockIdx.x / a.splits, sp = blockIdx.x - r * a.splits;
   constexpr int kSize = DT == DT_F32 ? 4 : 2, kVec = LpRegs<DT>::kVec;
@@ -244,59 +289,66 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(const __grid_c
   // values before the first 16-byte boundary and behind the last: one a thread
   const int pre = min(c1 - c0, (int)((16 - ((uintptr_t)(row + (size_t)c0 * kSize) & 15)) & 15) / kSize);
   const int v0 = c0 + pre, nv = (c1 - v0) / kVec, rest = (c1 - v0) - nv * kVec;
-  const uint4* body = reinterpret_cast<const uint4*>(row + (size_t)v0 * kSize);
+  const char* body = row + (size_t)v0 * kSize;
 
-  constexpr int kAhead = DT == DT_F32 ? 1 : 2;  // steps in flight: 64 bytes a thread
-  LpRegs<DT> cur, nxt[kAhead];
-  constexpr int kLoads = kLpEach / kVec;
+  constexpr int kLoads = kLpBytes / 16, kEach = LpRegs<DT>::kEach;
   constexpr uint32_t kNegInf = DT == DT_F32 ? 0xff800000u : DT == DT_BF16 ? 0xff80ff80u : 0xfc00fc00u;
-  auto load = [&](LpRegs<DT>& g, int at) {  // vectors at + j * 256 + t; -infinity behind the end
-#pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-      const int i = at + j * kLpThreads + t;
-      g.u[j] = i < nv ? __ldcs(body + i) : make_uint4(kNegInf, kNegInf, kNegInf, kNegInf);
-    }
+  constexpr int kStepVec = kLpThreads * kLoads, kStepBytes = kStepVec * 16;
+  const int steps = (nv + kStepVec - 1) / kStepVec;
+  auto fill = [&](int step) {  // one thread
+    const int bytes = min(kStepBytes, (nv - step * kStepVec) * 16);
+    uint64_t* bar = &sh.full[step % kLpStages];
+    mbar_arrive_expect_tx(bar, bytes);
+    bulk_copy_g2s(smem + (step % kLpStages) * kStepBytes, body + (size_t)step * kStepBytes, bytes, bar,
+                  l2_policy_evict_first());
   };
-  constexpr int kStepVec = kLpThreads * kLoads;
-  load(cur, 0);
-#pragma unroll
-  for (int i = 0; i < kAhead - 1; ++i) load(nxt[i], (i + 1) * kStepVec);
+  if (t == 0) {
+    for (int i = 0; i < kLpStages; ++i) mbar_init(&sh.full[i], 1);
+    fence_mbar_init();
+    sh.n = 0;
+    sh.abort = 0;
+    for (int i = 0; i < kLpStages && i < steps; ++i) fill(i);
+  }
+  __syncthreads();
 
   LpSum s = {-FLT_MAX, 0.f, 0.f};
   unsigned long long thr = 0;
   float thrv = -INFINITY;
-  if (TOP) {
-    if (t == 0) sh.n = 0;
-    __syncthreads();
-  }
-  int over = 0;
-  auto candidate = [&](float v, int i) {
+  int over = 0;  // the place of this thread's last candidate
+  auto candidate = [&](float v, int i, bool again) {
     const unsigned long long key = top_key(v, i);
-    if (key >= thr && key) {
-      const int at = atomicAdd(&sh.n, 1);
-      sh.buf[at] = key;
-      over = at;
-    }
+    if (key < thr || !key) return;
+    if (again)  // one of those kept already?
+#pragma unroll 1
+      for (int e = 0; e < 32; ++e)
+        if (sh.buf[e] == key) return;
+    over = atomicAdd(&sh.n, 1);
+    if (over < kLpBuf) sh.buf[over] = key;
   };
   if (t < pre + rest) {
     const int i = t < pre ? c0 + t : v0 + nv * kVec + (t - pre);
-    float x;
-    if constexpr (DT == DT_F32) x = reinterpret_cast<const float*>(row)[i];
-    else if constexpr (DT == DT_F16) x = __half2float(reinterpret_cast<const __half*>(row)[i]);
-    else x = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[i] << 16);
+    const float x = lp_value<DT>(row, i);
     if (x > s.m) s.m = x;
     s.add_diff(x - s.m);
-    if (TOP) candidate(x, i);
+    if (TOP) candidate(x, i, false);
   }
-  for (int at = 0; at < nv; at += kStepVec) {
-    if (at + kAhead * kStepVec < nv) load(nxt[kAhead - 1], at + kAhead * kStepVec);
+  for (int step = 0; step < steps; ++step) {
+    const int at = step * kStepVec;
+    const bool ok = mbar_wait_bounded(&sh.full[step % kLpStages], (step / kLpStages) & 1, a.timeout_ns);
+    if (!ok) sh.abort = 1;
+    LpRegs<DT> cur;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {  // -infinity behind the end
+      cur.u[j] = reinterpret_cast<const uint4*>(smem + (step % kLpStages) * kStepBytes)[j * kLpThreads + t];
+      if (at + j * kLpThreads + t >= nv) cur.u[j] = make_uint4(kNegInf, kNegInf, kNegInf, kNegInf);
+    }
     const float mx = cur.largest();
     if (mx > s.m) s.raise(mx);
     {
       const float nm = -s.m;
       float2 z = make_float2(0.f, 0.f), e2 = z;
 #pragma unroll
-      for (int i = 0; i < kLpEach; i += 2) {
+      for (int i = 0; i < kEach; i += 2) {
         const float2 y = make_float2(max_nan(cur.diff(i, nm), kLpFar) * kLog2e,
                                      max_nan(cur.diff(i + 1, nm), kLpFar) * kLog2e);
         const float2 e = make_float2(lp_exp2(y.x), lp_exp2(y.y));
@@ -308,53 +360,74 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(const __grid_c
     }
     if (TOP) {
       if (at == 0) {
-        // the threads' best values, over what the candidates will hold
-        unsigned long long best = 0;
+        // the k-th of the threads' largest values: at least k values reach it
+        const uint32_t u = __float_as_uint(mx + 0.f);
+        uint32_t top = mx == mx ? (u & 0x80000000u ? ~u : u | 0x80000000u) : 0u;
+        top = lp_sort(top, lane);
+        uint32_t* lists = reinterpret_cast<uint32_t*>(sh.list);
 #pragma unroll
-        for (int i = 0; i < kLpEach; ++i) {
-          const int e = v0 + ((i / kVec) * kLpThreads + t) * kVec + i % kVec;
-          const float v = cur.value(i);
-          const unsigned long long key = v == mx && (i / kVec) * kLpThreads + t < nv ? top_key(v, e) : 0;
-          best = key > best ? key : best;
+        for (int o = 1; o < kLpWarps; o <<= 1) {
+          if ((warp & (2 * o - 1)) == o) lists[warp * 32 + lane] = top;
+          __syncthreads();
+          if (!(warp & (2 * o - 1))) top = lp_merge(top, lists[(warp + o) * 32 + lane], lane);
         }
-        const int have = sh.n;  // the odd values at the ends, kept behind
-        unsigned long long odd = 0;
+        if (warp == 0 && lane == a.k - 1) sh.thr = (unsigned long long)top << 32;
         __syncthreads();
-        if (t < have) odd = sh.buf[t];
-        __syncthreads();
-        sh.buf[t] = best;
-        __syncthreads();
-        lp_compact(sh, kLpThreads, a.k, 0);
         thr = sh.thr;
-        thrv = thr ? key_value(thr) : -INFINITY;
-        __syncthreads();
-        if (t < have) sh.buf[t] = odd;
-        if (t == 0) sh.n = have;
-        __syncthreads();
-      }
-      if (mx >= thrv) {
-#pragma unroll
-        for (int i = 0; i < kLpEach; ++i) {
-          const float v = cur.value(i);
-          const int vec = at + (i / kVec) * kLpThreads + t;
-          if (v >= thrv && vec < nv) candidate(v, v0 + vec * kVec + i % kVec);
-        }
-      }
-      if (__syncthreads_or(over >= kLpCompact)) {
-        lp_compact(sh, sh.n, a.k, 1);
-        thr = sh.thr;
-        thrv = thr ? key_value(thr) : -INFINITY;
-        over = 0;
-        __syncthreads();
+        thrv = thr >> 32 ? key_value(thr) : -INFINITY;
       }
     }
-    cur = nxt[0];
+    // one barrier a step: the stage is free again, and whether the candidates
+    // are many (more than there is room for: their best raise the bound, and
+    // the step's values are gone through again) or a wait ran out
+    bool again = false;
+    do {
+      if (TOP && mx >= thrv) {
+        const uint32_t packed = LpRegs<DT>::pack_down(thrv);
+        uint32_t hits = 0;
 #pragma unroll
-    for (int i = 1; i < kAhead; ++i) nxt[i - 1] = nxt[i];
+        for (int i = 0; i < kEach / 2; ++i)
+          if (cur.pair_reaches(i, thrv, packed)) hits |= 1u << i;
+        while (hits) {  // few: from the ring again, so that this code is there once
+          const int i = 2 * (__ffs(hits) - 1), vec = i / kVec * kLpThreads + t;
+          hits &= hits - 1;
+          if (at + vec >= nv) continue;
+          const char* w = reinterpret_cast<const char*>(smem) + (step % kLpStages) * kStepBytes +
+                          vec * 16 + i % kVec * kSize;
+#pragma unroll 1
+          for (int e = 0; e < 2; ++e)
+            candidate(lp_value<DT>(w, e), v0 + (at + vec) * kVec + i % kVec + e, again);
+        }
+      }
+      again = false;
+      if (__syncthreads_or(!ok || (TOP && over >= kLpCompact))) {
+        if (sh.abort) {
+          if (t == 0) {
+            atomicExch(a.err, (int)DERR_TIMEOUT);
+            for (int i = step; i < steps && i < step + kLpStages; ++i)  // copies under way
+              mbar_wait_bounded(&sh.full[i % kLpStages], (i / kLpStages) & 1, a.timeout_ns);
+          }
+          return;
+        }
+        if (TOP) {
+          const int n = sh.n;
+          again = n > kLpBuf;
+          lp_compact(sh, sh.buf, min(n, kLpBuf), a.k, 1);
+          thr = sh.thr;
+          thrv = thr >> 32 ? key_value(thr) : -INFINITY;
+          over = 0;
+          __syncthreads();
+        }
+      }
+    } while (TOP && again);
+    if (t == 0 && step + kLpStages < steps) {
+      fence_proxy_async_smem();  // the reads of this stage before the copy into it
+      fill(step + kLpStages);
+    }
   }
   if (TOP) {
     __syncthreads();
-    lp_compact(sh, sh.n, a.k, 1);
+    lp_compact(sh, sh.buf, sh.n, a.k, 1);
   }
   s.join_lanes(32);
   if (lane == 0) sh.sums[warp] = s;
@@ -379,7 +452,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(const __grid_c
     // the row's last CTA: the splits' sums in their order, and the best of
     // their best
     if (warp == 0) {
-      static_assert(kLpSplits == 64, "two splits a lane");
+      static_assert(kLpSplits <= 64, "two splits a lane");
       const float4 v = lane < a.splits ? __ldcg(a.stat + at + lane) : make_float4(-FLT_MAX, 0.f, 0.f, 0.f);
       const float4 w =
           lane + 32 < a.splits ? __ldcg(a.stat + at + lane + 32) : make_float4(-FLT_MAX, 0.f, 0.f, 0.f);
@@ -389,9 +462,11 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(const __grid_c
     }
     if (TOP) {
       const int n = a.splits * a.k;
-      for (int i = t; i < n; i += kLpThreads) sh.buf[i] = __ldcg(a.keys + at * a.k + i);
+      // (the ring's copies are all done and read)
+      unsigned long long* all = reinterpret_cast<unsigned long long*>(smem);
+      for (int i = t; i < n; i += kLpThreads) all[i] = __ldcg(a.keys + at * a.k + i);
       __syncthreads();
-      lp_compact(sh, n, a.k, 1);
+      lp_compact(sh, all, n, a.k, 1);
     }
   }
   if (warp > 0) return;
@@ -406,11 +481,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_token_logprobs(const __grid_c
         atomicExch(a.err, kDerrBadToken);
         lp = NAN;
       } else if (i >= 0) {
-        float x;
-        if constexpr (DT == DT_F32) x = reinterpret_cast<const float*>(row)[i];
-        else if constexpr (DT == DT_F16) x = __half2float(reinterpret_cast<const __half*>(row)[i]);
-        else x = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[i] << 16);
-        lp = x - s.m - lz;
+        lp = lp_value<DT>(row, i) - s.m - lz;
       }
       a.logprob[r] = lp;
     }
@@ -439,6 +510,31 @@ static void lp_split(int rows, int V, int& splits, int& chunk) {
 constexpr size_t kLpTick = (kLpCtas / 2 * 4 + 255) / 256 * 256;
 
 static size_t lp_align(size_t v) { return (v + 255) / 256 * 256; }
+
+constexpr int kLpSmemTop = kLpRing + (int)sizeof(LpShared);
+constexpr int kLpSmem = kLpRing + (int)offsetof(LpShared, buf);
+
+// The kernels' shared memory, once per device.
+static cudaError_t lp_setup() {
+  constexpr int kMaxDev = 64;
+  static std::mutex mu;
+  static bool ready[kMaxDev] = {false};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lk(mu);
+  if (ready[dev]) return cudaSuccess;
+  auto set = [&](const void* f) {
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kLpSmemTop);
+  };
+  set((const void*)k_token_logprobs<DT_F32, true>);
+  set((const void*)k_token_logprobs<DT_BF16, true>);
+  set((const void*)k_token_logprobs<DT_F16, true>);
+  ready[dev] = e == cudaSuccess;
+  return e;
+}
 
 }  // namespace ws
 
@@ -481,8 +577,14 @@ ws_status ws_token_logprobs(const void *logits, int dtype, long long ld, const i
     set_error("workspace too small: need %zu bytes, got %zu", need, workspace_bytes);
     return WS_ERR_ARG;
   }
+  cudaError_t e = lp_setup();
+  if (e != cudaSuccess) {
+    set_error("log-probabilities setup failed: %s", cudaGetErrorString(e));
+    return WS_ERR_CUDA;
+  }
   LogprobParams a = {};
   a.x = logits;
+  a.timeout_ns = tuning().timeout_ns;
   a.targets = targets;
   a.logprob = logprob;
   a.entropy = entropy;
@@ -504,7 +606,7 @@ ws_status ws_token_logprobs(const void *logits, int dtype, long long ld, const i
   a.keys = reinterpret_cast<unsigned long long*>(w + lp_align((size_t)rows * a.splits * 16));
   cudaStream_t st = (cudaStream_t)stream;
   const int grid = rows * a.splits;
-  const int sm = sizeof(LpShared);
+  const int sm = topk ? kLpSmemTop : kLpSmem;
   if (dtype == WS_DTYPE_F32) {
     if (topk) k_token_logprobs<DT_F32, true><<<grid, kLpThreads, sm, st>>>(a);
     else k_token_logprobs<DT_F32, false><<<grid, kLpThreads, sm, st>>>(a);
@@ -515,7 +617,7 @@ ws_status ws_token_logprobs(const void *logits, int dtype, long long ld, const i
     if (topk) k_token_logprobs<DT_F16, true><<<grid, kLpThreads, sm, st>>>(a);
     else k_token_logprobs<DT_F16, false><<<grid, kLpThreads, sm, st>>>(a);
   }
-  const cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("launch failed: %s", cudaGetErrorString(e));
     return WS_ERR_CUDA;
