@@ -24,7 +24,6 @@ constexpr int kQ4MinTiles = 1 * kQ4Warps;            // tiles a CTA takes at lea
 constexpr int kQ4Merge = 16;                         // partial results merged in one go
 constexpr int kQ4Part = kKvDim + 4;                  // one partial result: acc[128], max, sum, two unused
 constexpr int kQ4Ring = kQ4Warps * kQ4Stages * kQ4StageBytes;
-constexpr int kQ4Smem = kQ4Ring + kQ4Warps * kQ4MaxG * kKvDim * 4;
 // the running maximum follows the tile's only when that is 2^8 above it
 constexpr float kQ4Lazy = 8.f;
 
@@ -201,16 +200,406 @@ __device__ __forceinline__ void q4_put(float* e, int lane, float4 O, float M, fl
   if (lane == 0) *reinterpret_cast<float2*>(e + kKvDim) = make_float2(M, L);
 }
 
-__global__ void __launch_bounds__(kQ4Threads, 2)
+// The two products of a warp and what it accumulates, for up to 8 heads a group:
+// heads are the rows of the products, their hi terms in rows 0..7 and their lo
+// terms in rows 8..15; the columns are slots, then dimensions.
+struct Q4Wide {
+  static constexpr int kHeads = 8;
+  static constexpr int kCtas = 2;  // a SM: 245 registers; three (168, spilled) took 78 us where this takes 73.5
+  struct Shared {
+    uint4 qfrag[8][32];
+    float qsum[kHeads][4];
+  };
+  float o[16][4], m;
+  float zo[4];  // sum p z, column = group (the columns 4 .. 7 repeat them)
+  float2 l;
+  uint32_t qz[2], zmask;
+
+  __device__ __forceinline__ void begin(const AttnQ4Params& a, int b, int g0, Shared& sh) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rg = lane >> 2, rt = lane & 3;
+    // the queries as the first product's A operand, in shared memory (held in
+    // registers they cost a CTA a SM its place): head rg in rows rg (hi terms)
+    // and rg + 8 (lo terms); lane rt of a quad holds dimensions 32 g + 8 rt ..
+    // + 7, in the order of the key row's nibbles; warp g makes group g's.  qz:
+    // their sums per group, the operand against the zeros (k = group)
+    {
+      static_assert(kQ4Warps == 4, "a warp per group");
+      const float* qr = a.q + ((size_t)b * a.nh + (size_t)g0 * a.G + (rg < a.G ? rg : 0)) * kKvDim;
+      float v[8], sum = 0.f;
+      load8<DT_F32>(qr + 32 * warp + 8 * rt, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = rg < a.G ? v[i] * a.scale : 0.f;
+        sum += v[i];
+        v[i] *= i & 1 ? kQ4Hi : kQ4Lo;
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      if (rt == 0) sh.qsum[rg][warp] = sum;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint4 f;
+        q4_split(v[2 * k], v[2 * k + 4], f.x, f.y);
+        q4_split(v[2 * k + 1], v[2 * k + 5], f.z, f.w);
+        sh.qfrag[2 * warp + k][lane] = f;
+      }
+    }
+    __syncthreads();
+    {
+      const float2 z = rt < 2 ? *reinterpret_cast<const float2*>(&sh.qsum[rg][2 * rt]) : make_float2(0.f, 0.f);
+      q4_split(z.x, z.y, qz[0], qz[1]);
+    }
+    zmask = rt < 2 ? 0xffffffffu : 0u;
+    m = -1e30f;
+    l = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) zo[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+  }
+
+  __device__ __forceinline__ void tile(const unsigned char* st, int slot0, int pos, const Shared& sh) {
+    const int lane = threadIdx.x & 31, rg = lane >> 2, rt = lane & 3;
+    // scores: head rg, slots 8 n + 2 rt + e
+    float2 s[4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint4 kw[2], ks[2][2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const unsigned char* kr = st + (16 * u + 8 * n + rg) * kKvRow;
+        kw[n] = *reinterpret_cast<const uint4*>(kr + 16 * rt);
+        const uint2 kz = *reinterpret_cast<const uint2*>(kr + kKvCodes + 8 * (rt & 1));
+        const unsigned char* ksp = st + (16 * u + 8 * n + 2 * rt) * kKvRow + kKvCodes;
+        ks[n][0] = *reinterpret_cast<const uint4*>(ksp);
+        ks[n][1] = *reinterpret_cast<const uint4*>(ksp + kKvRow);
+        float cz[4];
+        q4_mma0(cz, qz[0], qz[1], 0u, 0u, __byte_perm(kz.x, kz.y, 0x7632) & zmask, 0u);
+        s[2 * u + n] = add2(make_float2(cz[0], cz[1]), make_float2(cz[2], cz[3]));
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const uint4 q0 = sh.qfrag[2 * g][lane], q1 = sh.qfrag[2 * g + 1][lane];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const uint32_t w = reinterpret_cast<const uint32_t*>(&kw[n])[g], w8 = w >> 8;
+          float c[4];
+          q4_mma0(c, q0.x, q0.y, q0.z, q0.w, q4_pair<0>(w), q4_pair<1>(w));
+          mma_bf16_16816(c, q1.x, q1.y, q1.z, q1.w, q4_pair<0>(w8), q4_pair<1>(w8));
+          s[2 * u + n] = fma2(make_float2(bf16lo(reinterpret_cast<const uint32_t*>(&ks[n][0])[g]),
+                                          bf16lo(reinterpret_cast<const uint32_t*>(&ks[n][1])[g])),
+                              add2(make_float2(c[0], c[1]), make_float2(c[2], c[3])),
+                              s[2 * u + n]);
+        }
+      }
+    }
+    if (slot0 + kQ4Tile > pos + 1) {
+      const int slot = slot0 + 2 * rt;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        if (slot + 8 * n > pos) s[n].x = -INFINITY;
+        if (slot + 8 * n + 1 > pos) s[n].y = -INFINITY;
+      }
+    }
+    float mx = fmaxf(fmaxf(fmaxf(s[0].x, s[0].y), fmaxf(s[1].x, s[1].y)),
+                     fmaxf(fmaxf(s[2].x, s[2].y), fmaxf(s[3].x, s[3].y)));
+    if (__any_sync(0xffffffffu, mx > m + kQ4Lazy)) {
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float mn = fmaxf(m, mx), f = q4_exp2(m - mn);
+      m = mn;
+      l.x *= f, l.y *= f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) zo[e] *= f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] *= f;
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      s[n].x = q4_exp2(s[n].x - m);
+      s[n].y = q4_exp2(s[n].y - m);
+      l = add2(l, s[n]);
+    }
+    // output: the probabilities times each slot's scale enter as the A
+    // operand (hi rows and lo rows again), the codes as B: column rg is
+    // dimension 32 g + 4 rg + i
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const unsigned char* sv = st + (kQ4Tile + 16 * u + 2 * rt) * kKvRow;
+      uint2 vw[2][2];
+      uint4 vs[2][2];
+      uint32_t ph[2], pl[2], bz[2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        uint32_t z[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const unsigned char* r = sv + (8 * n + e) * kKvRow;
+          vw[n][e] = *reinterpret_cast<const uint2*>(r + 8 * rg);
+          vs[n][e] = *reinterpret_cast<const uint4*>(r + kKvCodes);
+          z[e] = *reinterpret_cast<const uint32_t*>(r + kKvCodes + 4 * (rg & 3));
+        }
+        bz[n] = __byte_perm(z[0], z[1], 0x7632);
+        q4_split(s[2 * u + n].x, s[2 * u + n].y, ph[n], pl[n]);
+      }
+      mma_bf16_16816(zo, ph[0], pl[0], ph[1], pl[1], bz[0], bz[1]);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        uint32_t ah[2], al[2], m0[2], m1[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const uint32_t z0 = reinterpret_cast<const uint32_t*>(&vs[n][0])[g];
+          const uint32_t z1 = reinterpret_cast<const uint32_t*>(&vs[n][1])[g];
+          const float2 ps = mul2(s[2 * u + n], make_float2(bf16lo(z0), bf16lo(z1)));
+          q4_split(ps.x, ps.y, ah[n], al[n]);
+          const uint32_t w0 = g < 2 ? vw[n][0].x : vw[n][0].y, w1 = g < 2 ? vw[n][1].x : vw[n][1].y;
+          m0[n] = __byte_perm(w0, w1, g & 1 ? 0x0602 : 0x0400);
+          m1[n] = __byte_perm(w0, w1, g & 1 ? 0x0703 : 0x0501);
+        }
+        mma_bf16_16816(o[4 * g], ah[0], al[0], ah[1], al[1], q4_pair<0>(m0[0]), q4_pair<0>(m0[1]));
+        mma_bf16_16816(o[4 * g + 1], ah[0], al[0], ah[1], al[1], q4_pair<1>(m0[0]), q4_pair<1>(m0[1]));
+        mma_bf16_16816(o[4 * g + 2], ah[0], al[0], ah[1], al[1], q4_pair<0>(m1[0]), q4_pair<0>(m1[1]));
+        mma_bf16_16816(o[4 * g + 3], ah[0], al[0], ah[1], al[1], q4_pair<1>(m1[0]), q4_pair<1>(m1[1]));
+      }
+    }
+  }
+
+  // this warp's result: cm, cl [heads], comb [heads][128]
+  __device__ __forceinline__ void end(int G, float* cm, float* cl, float* comb) {
+    const int lane = threadIdx.x & 31, rg = lane >> 2, rt = lane & 3;
+    // dimensions 32 g + 8 rt .. + 7
+    float lsum = l.x + l.y, zs[4];
+    lsum += __shfl_xor_sync(0xffffffffu, lsum, 1);
+    lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      zs[g] = __shfl_sync(0xffffffffu, zo[g & 1] + zo[2 + (g & 1)], (lane & 28) + (g >> 1));
+    if (rt == 0) cm[rg] = m, cl[rg] = lsum;
+    float* cw = comb + rg * kKvDim + 8 * rt;
+    if (rg < G) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float4*>(cw + 32 * g + 4 * e) =
+              make_float4(fmaf(o[4 * g + 0][e] + o[4 * g + 0][2 + e], kQ4Lo, zs[g]),
+                          fmaf(o[4 * g + 1][e] + o[4 * g + 1][2 + e], kQ4Hi, zs[g]),
+                          fmaf(o[4 * g + 2][e] + o[4 * g + 2][2 + e], kQ4Lo, zs[g]),
+                          fmaf(o[4 * g + 3][e] + o[4 * g + 3][2 + e], kQ4Hi, zs[g]));
+    }
+  }
+};
+
+__device__ __forceinline__ uint32_t q4_transpose(uint32_t a) {  // an 8x8 matrix of 16-bit values
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+// The same for up to 4 heads a group, with the operands changed over: the codes
+// are the rows (16 slots, then 16 dimensions), the columns the heads' hi terms
+// and, from 4 on, their lo terms.  Half as many products and accumulators, so
+// that twice the CTAs fit; the probabilities pass from rows to columns by a
+// transposition between the two products.
+struct Q4Narrow {
+  static constexpr int kHeads = 4;
+  static constexpr int kCtas = 3;
+  struct Shared {};
+  // lane: heads 2 (rt & 1) + e; o[2 g + i / 2]: dimensions 32 g + 4 rg + i, hi
+  // terms for rt < 2, lo terms for the others
+  float o[8][4], zo[4][2], m[2], l[2];
+  uint32_t qb[8][2], qz;
+
+  __device__ __forceinline__ void begin(const AttnQ4Params& a, int b, int g0, Shared&) {
+    const int lane = threadIdx.x & 31, rg = lane >> 2, rt = lane & 3;
+    const int h = rg & 3;  // column rg: head h's hi term, or its lo term
+    const float* qr = a.q + ((size_t)b * a.nh + (size_t)g0 * a.G + (h < a.G ? h : 0)) * kKvDim;
+    float sums[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      float v[8], sum = 0.f;
+      load8<DT_F32>(qr + 32 * g + 8 * rt, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = h < a.G ? v[i] * a.scale : 0.f;
+        sum += v[i];
+        v[i] *= i & 1 ? kQ4Hi : kQ4Lo;
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      sums[g] = sum;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint32_t hi, lo;
+        q4_split(v[2 * k], v[2 * k + 4], hi, lo);
+        qb[2 * g + k][0] = rg < 4 ? hi : lo;
+        q4_split(v[2 * k + 1], v[2 * k + 5], hi, lo);
+        qb[2 * g + k][1] = rg < 4 ? hi : lo;
+      }
+    }
+    uint32_t hi, lo;
+    q4_split(rt == 0 ? sums[0] : rt == 1 ? sums[2] : 0.f, rt == 0 ? sums[1] : rt == 1 ? sums[3] : 0.f,
+             hi, lo);
+    qz = rg < 4 ? hi : lo;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) m[e] = -1e30f, l[e] = 0.f;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) zo[g][0] = zo[g][1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+  }
+
+  __device__ __forceinline__ void tile(const unsigned char* st, int slot0, int pos, const Shared&) {
+    const int lane = threadIdx.x & 31, rg = lane >> 2, rt = lane & 3;
+    const uint32_t zmask = rt < 2 ? 0xffffffffu : 0u;
+    // scores: slots 16 u + 8 n + rg, heads 2 (rt & 1) + e
+    float s[2][2][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint4 kw[2], ks[2];
+      uint32_t z[2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const unsigned char* r = st + (16 * u + 8 * n + rg) * kKvRow;
+        kw[n] = *reinterpret_cast<const uint4*>(r + 16 * rt);
+        ks[n] = *reinterpret_cast<const uint4*>(r + kKvCodes);
+        z[n] = (rt & 1 ? __byte_perm(ks[n].z, ks[n].w, 0x7632) : __byte_perm(ks[n].x, ks[n].y, 0x7632)) &
+               zmask;
+      }
+      float sum[4];
+      q4_mma0(sum, z[0], z[1], 0u, 0u, qz, 0u);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const uint32_t w0 = reinterpret_cast<const uint32_t*>(&kw[0])[g];
+        const uint32_t w1 = reinterpret_cast<const uint32_t*>(&kw[1])[g];
+        float c[4];
+        q4_mma0(c, q4_pair<0>(w0), q4_pair<0>(w1), q4_pair<1>(w0), q4_pair<1>(w1), qb[2 * g][0], qb[2 * g][1]);
+        mma_bf16_16816(c, q4_pair<0>(w0 >> 8), q4_pair<0>(w1 >> 8), q4_pair<1>(w0 >> 8),
+                       q4_pair<1>(w1 >> 8), qb[2 * g + 1][0], qb[2 * g + 1][1]);
+        const float s0 = bf16lo(reinterpret_cast<const uint32_t*>(&ks[0])[g]);
+        const float s1 = bf16lo(reinterpret_cast<const uint32_t*>(&ks[1])[g]);
+        sum[0] = fmaf(s0, c[0], sum[0]);
+        sum[1] = fmaf(s0, c[1], sum[1]);
+        sum[2] = fmaf(s1, c[2], sum[2]);
+        sum[3] = fmaf(s1, c[3], sum[3]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // hi and lo terms
+        s[u][i >> 1][i & 1] = sum[i] + __shfl_xor_sync(0xffffffffu, sum[i], 2);
+    }
+    if (slot0 + kQ4Tile > pos + 1) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          if (slot0 + 16 * u + 8 * n + rg > pos) s[u][n][0] = s[u][n][1] = -INFINITY;
+    }
+    float mx[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) mx[e] = fmaxf(fmaxf(s[0][0][e], s[0][1][e]), fmaxf(s[1][0][e], s[1][1][e]));
+    if (__any_sync(0xffffffffu, mx[0] > m[0] + kQ4Lazy || mx[1] > m[1] + kQ4Lazy)) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int i = 4; i < 32; i <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], i));
+        const float mn = fmaxf(m[e], mx[e]), f = q4_exp2(m[e] - mn);
+        m[e] = mn;
+        l[e] *= f;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) zo[g][e] *= f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i][e] *= f, o[i][2 + e] *= f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          s[u][n][e] = q4_exp2(s[u][n][e] - m[e]);
+          l[e] += s[u][n][e];
+        }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const unsigned char* sv = st + (kQ4Tile + 16 * u) * kKvRow;
+      uint2 vw[2][2];
+      uint4 vs[2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          vw[n][e] = *reinterpret_cast<const uint2*>(sv + (8 * n + 2 * rt + e) * kKvRow + 8 * rg);
+        vs[n] = *reinterpret_cast<const uint4*>(sv + (8 * n + rg) * kKvRow + kKvCodes);
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        uint32_t pb[2], m0[2], m1[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const uint32_t sz = reinterpret_cast<const uint32_t*>(&vs[n])[g];
+          const float sc = bf16lo(sz), z = bf16hi(sz);
+          uint32_t hi, lo;
+          q4_split(s[u][n][0] * sc, s[u][n][1] * sc, hi, lo);
+          pb[n] = q4_transpose(rt < 2 ? hi : lo);
+          zo[g][0] = fmaf(s[u][n][0], z, zo[g][0]);
+          zo[g][1] = fmaf(s[u][n][1], z, zo[g][1]);
+          const uint32_t w0 = g < 2 ? vw[n][0].x : vw[n][0].y, w1 = g < 2 ? vw[n][1].x : vw[n][1].y;
+          m0[n] = __byte_perm(w0, w1, g & 1 ? 0x0602 : 0x0400);
+          m1[n] = __byte_perm(w0, w1, g & 1 ? 0x0703 : 0x0501);
+        }
+        mma_bf16_16816(o[2 * g], q4_pair<0>(m0[0]), q4_pair<1>(m0[0]), q4_pair<0>(m0[1]),
+                       q4_pair<1>(m0[1]), pb[0], pb[1]);
+        mma_bf16_16816(o[2 * g + 1], q4_pair<0>(m1[0]), q4_pair<1>(m1[0]), q4_pair<0>(m1[1]),
+                       q4_pair<1>(m1[1]), pb[0], pb[1]);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void end(int G, float* cm, float* cl, float* comb) {
+    const int lane = threadIdx.x & 31, rg = lane >> 2, rt = lane & 3;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int i = 4; i < 32; i <<= 1) {
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], i);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) zo[g][e] += __shfl_xor_sync(0xffffffffu, zo[g][e], i);
+      }
+      if (rg == 0 && rt < 2) cm[2 * rt + e] = m[e], cl[2 * rt + e] = l[e];
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = o[2 * g + (i >> 1)][2 * (i & 1) + e];
+          v[i] = fmaf(x + __shfl_xor_sync(0xffffffffu, x, 2), i & 1 ? kQ4Hi : kQ4Lo, zo[g][e]);
+        }
+        if (rt < 2 && 2 * rt + e < G)
+          *reinterpret_cast<float4*>(comb + (2 * rt + e) * kKvDim + 32 * g + 4 * rg) =
+              make_float4(v[0], v[1], v[2], v[3]);
+      }
+  }
+};
+
+template <class Core>
+__global__ void __launch_bounds__(kQ4Threads, Core::kCtas)
     k_decode_attention_q4(const __grid_constant__ AttnQ4Params a) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t full[kQ4Warps][kQ4Stages];
-  __shared__ float cm[kQ4Warps][kQ4MaxG], cl[kQ4Warps][kQ4MaxG];
-  __shared__ uint4 qfrag[8][32];
-  __shared__ float qsum[kQ4MaxG][4];
+  __shared__ float cm[kQ4Warps][Core::kHeads], cl[kQ4Warps][Core::kHeads];
+  __shared__ typename Core::Shared shared;
   __shared__ int last;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, G = a.G;
-  const int rg = lane >> 2, rt = lane & 3;  // row and column of the fragments
 
   // the tiles of all rows and heads, cut into as many equal runs as there are
   // CTAs; every warp finds the run's place by itself
@@ -303,49 +692,8 @@ __global__ void __launch_bounds__(kQ4Threads, 2)
   while (x0 < run) {  // one (row, head) at a time
     q4_seek(a, cur, x0);
     const int x1 = min(run, cur.at + cur.nt);
-    // the queries as the first product's A operand, in shared memory (held in
-    // registers they cost a CTA a SM its place): head rg in rows rg (hi terms)
-    // and rg + 8 (lo terms); lane rt of a quad holds dimensions 32 g + 8 rt ..
-    // + 7, in the order of the key row's nibbles; warp g makes group g's.  qz:
-    // their sums per group, the operand against the zeros (k = group)
-    {
-      static_assert(kQ4Warps == 4, "a warp per group");
-      const float* qr = a.q + ((size_t)cur.b * a.nh + (size_t)cur.g * G + (rg < G ? rg : 0)) * kKvDim;
-      float v[8], sum = 0.f;
-      load8<DT_F32>(qr + 32 * warp + 8 * rt, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = rg < G ? v[i] * a.scale : 0.f;
-        sum += v[i];
-        v[i] *= i & 1 ? kQ4Hi : kQ4Lo;
-      }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      if (rt == 0) qsum[rg][warp] = sum;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint4 f;
-        q4_split(v[2 * k], v[2 * k + 4], f.x, f.y);
-        q4_split(v[2 * k + 1], v[2 * k + 5], f.z, f.w);
-        qfrag[2 * warp + k][lane] = f;
-      }
-    }
-    __syncthreads();
-    uint32_t qz[2];
-    {
-      const float2 z = rt < 2 ? *reinterpret_cast<const float2*>(&qsum[rg][2 * rt]) : make_float2(0.f, 0.f);
-      q4_split(z.x, z.y, qz[0], qz[1]);
-    }
-    const uint32_t zmask = rt < 2 ? 0xffffffffu : 0u;
-    float o[16][4], m = -1e30f;
-    // zo: sum p z, column = group (the columns 4 .. 7 repeat them)
-    float zo[4] = {0.f, 0.f, 0.f, 0.f};
-    float2 l = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-
+    Core core;
+    core.begin(a, cur.b, cur.g, shared);
     for (; x < x1; x += kQ4Warps) {
       const unsigned char* st = ring + nc * kQ4StageBytes;
       bool ok = abort || mbar_try_wait(&full[warp][nc], par);
@@ -356,137 +704,14 @@ __global__ void __launch_bounds__(kQ4Threads, 2)
           if (lane == 0) atomicExch(a.err, (int)DERR_TIMEOUT);
         }
       }
-      if (!abort) {
-        // scores: head rg, slots 8 n + 2 rt + e
-        float2 s[4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          uint4 kw[2], ks[2][2];
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const unsigned char* kr = st + (16 * u + 8 * n + rg) * kKvRow;
-            kw[n] = *reinterpret_cast<const uint4*>(kr + 16 * rt);
-            const uint2 kz = *reinterpret_cast<const uint2*>(kr + kKvCodes + 8 * (rt & 1));
-            const unsigned char* ksp = st + (16 * u + 8 * n + 2 * rt) * kKvRow + kKvCodes;
-            ks[n][0] = *reinterpret_cast<const uint4*>(ksp);
-            ks[n][1] = *reinterpret_cast<const uint4*>(ksp + kKvRow);
-            float cz[4];
-            q4_mma0(cz, qz[0], qz[1], 0u, 0u, __byte_perm(kz.x, kz.y, 0x7632) & zmask, 0u);
-            s[2 * u + n] = add2(make_float2(cz[0], cz[1]), make_float2(cz[2], cz[3]));
-          }
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const uint4 q0 = qfrag[2 * g][lane], q1 = qfrag[2 * g + 1][lane];
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const uint32_t w = reinterpret_cast<const uint32_t*>(&kw[n])[g], w8 = w >> 8;
-              float c[4];
-              q4_mma0(c, q0.x, q0.y, q0.z, q0.w, q4_pair<0>(w), q4_pair<1>(w));
-              mma_bf16_16816(c, q1.x, q1.y, q1.z, q1.w, q4_pair<0>(w8), q4_pair<1>(w8));
-              s[2 * u + n] = fma2(make_float2(bf16lo(reinterpret_cast<const uint32_t*>(&ks[n][0])[g]),
-                                              bf16lo(reinterpret_cast<const uint32_t*>(&ks[n][1])[g])),
-                                  add2(make_float2(c[0], c[1]), make_float2(c[2], c[3])),
-                                  s[2 * u + n]);
-            }
-          }
-        }
-        if ((x - cur.at + 1) * kQ4Tile > cur.pos + 1) {
-          const int slot = (x - cur.at) * kQ4Tile + 2 * rt;
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            if (slot + 8 * n > cur.pos) s[n].x = -INFINITY;
-            if (slot + 8 * n + 1 > cur.pos) s[n].y = -INFINITY;
-          }
-        }
-        float mx = fmaxf(fmaxf(fmaxf(s[0].x, s[0].y), fmaxf(s[1].x, s[1].y)),
-                         fmaxf(fmaxf(s[2].x, s[2].y), fmaxf(s[3].x, s[3].y)));
-        if (__any_sync(0xffffffffu, mx > m + kQ4Lazy)) {
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float mn = fmaxf(m, mx), f = q4_exp2(m - mn);
-          m = mn;
-          l.x *= f, l.y *= f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) zo[e] *= f;
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][e] *= f;
-        }
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          s[n].x = q4_exp2(s[n].x - m);
-          s[n].y = q4_exp2(s[n].y - m);
-          l = add2(l, s[n]);
-        }
-        // output: the probabilities times each slot's scale enter as the A
-        // operand (hi rows and lo rows again), the codes as B: column rg is
-        // dimension 32 g + 4 rg + i
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const unsigned char* sv = st + (kQ4Tile + 16 * u + 2 * rt) * kKvRow;
-          uint2 vw[2][2];
-          uint4 vs[2][2];
-          uint32_t ph[2], pl[2], bz[2];
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            uint32_t z[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const unsigned char* r = sv + (8 * n + e) * kKvRow;
-              vw[n][e] = *reinterpret_cast<const uint2*>(r + 8 * rg);
-              vs[n][e] = *reinterpret_cast<const uint4*>(r + kKvCodes);
-              z[e] = *reinterpret_cast<const uint32_t*>(r + kKvCodes + 4 * (rg & 3));
-            }
-            bz[n] = __byte_perm(z[0], z[1], 0x7632);
-            q4_split(s[2 * u + n].x, s[2 * u + n].y, ph[n], pl[n]);
-          }
-          mma_bf16_16816(zo, ph[0], pl[0], ph[1], pl[1], bz[0], bz[1]);
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            uint32_t ah[2], al[2], m0[2], m1[2];
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const uint32_t z0 = reinterpret_cast<const uint32_t*>(&vs[n][0])[g];
-              const uint32_t z1 = reinterpret_cast<const uint32_t*>(&vs[n][1])[g];
-              const float2 ps = mul2(s[2 * u + n], make_float2(bf16lo(z0), bf16lo(z1)));
-              q4_split(ps.x, ps.y, ah[n], al[n]);
-              const uint32_t w0 = g < 2 ? vw[n][0].x : vw[n][0].y, w1 = g < 2 ? vw[n][1].x : vw[n][1].y;
-              m0[n] = __byte_perm(w0, w1, g & 1 ? 0x0602 : 0x0400);
-              m1[n] = __byte_perm(w0, w1, g & 1 ? 0x0703 : 0x0501);
-            }
-            mma_bf16_16816(o[4 * g], ah[0], al[0], ah[1], al[1], q4_pair<0>(m0[0]), q4_pair<0>(m0[1]));
-            mma_bf16_16816(o[4 * g + 1], ah[0], al[0], ah[1], al[1], q4_pair<1>(m0[0]), q4_pair<1>(m0[1]));
-            mma_bf16_16816(o[4 * g + 2], ah[0], al[0], ah[1], al[1], q4_pair<0>(m1[0]), q4_pair<0>(m1[1]));
-            mma_bf16_16816(o[4 * g + 3], ah[0], al[0], ah[1], al[1], q4_pair<1>(m1[0]), q4_pair<1>(m1[1]));
-          }
-        }
-      }
+      if (!abort) core.tile(st, (x - cur.at) * kQ4Tile, cur.pos, shared);
       nc ^= 1;
       par ^= nc == 0;
       issue();
     }
 
-    // the four warps' results, then this CTA's: dimensions 32 g + 8 rt .. + 7
-    float lsum = l.x + l.y, zs[4];
-    lsum += __shfl_xor_sync(0xffffffffu, lsum, 1);
-    lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
-#pragma unroll
-    for (int g = 0; g < 4; ++g)
-      zs[g] = __shfl_sync(0xffffffffu, zo[g & 1] + zo[2 + (g & 1)], (lane & 28) + (g >> 1));
-    if (rt == 0) cm[warp][rg] = m, cl[warp][rg] = lsum;
-    float* cw = comb + ((size_t)warp * kQ4MaxG + rg) * kKvDim + 8 * rt;
-    if (rg < G) {
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<float4*>(cw + 32 * g + 4 * e) =
-              make_float4(fmaf(o[4 * g + 0][e] + o[4 * g + 0][2 + e], kQ4Lo, zs[g]),
-                          fmaf(o[4 * g + 1][e] + o[4 * g + 1][2 + e], kQ4Hi, zs[g]),
-                          fmaf(o[4 * g + 2][e] + o[4 * g + 2][2 + e], kQ4Lo, zs[g]),
-                          fmaf(o[4 * g + 3][e] + o[4 * g + 3][2 + e], kQ4Hi, zs[g]));
-    }
+    // the four warps' results, then this CTA's
+    core.end(G, cm[warp], cl[warp], comb + (size_t)warp * Core::kHeads * kKvDim);
     __syncthreads();
     const int seg0 = start + cur.at;  // the segment's first tile among all
     const int c0 = seg0 / per, n = (seg0 + cur.nt - 1) / per - c0 + 1;
@@ -501,7 +726,7 @@ __global__ void __launch_bounds__(kQ4Threads, 2)
 #pragma unroll
       for (int w = 0; w < kQ4Warps; ++w) {
         const float f = q4_exp2(cm[w][h] - M);
-        const float4 v = reinterpret_cast<const float4*>(comb + ((size_t)w * kQ4MaxG + h) * kKvDim)[lane];
+        const float4 v = reinterpret_cast<const float4*>(comb + ((size_t)w * Core::kHeads + h) * kKvDim)[lane];
         O.x = fmaf(f, v.x, O.x);
         O.y = fmaf(f, v.y, O.y);
         O.z = fmaf(f, v.z, O.z);
@@ -561,7 +786,11 @@ __global__ void __launch_bounds__(kQ4Threads, 2)
   }
 }
 
+template <class Core>
+constexpr int kQ4Smem = kQ4Ring + kQ4Warps * Core::kHeads * kKvDim * 4;
+
 // Resident CTAs of the device: the grid, set up once per device.
+template <class Core>
 static int q4_grid(cudaError_t* err) {
   constexpr int kMaxDev = 64;
   static std::mutex mu;
@@ -577,11 +806,11 @@ static int q4_grid(cudaError_t* err) {
     int sms = 0, per_sm = 0;
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k_decode_attention_q4, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               kQ4Smem);
+      e = cudaFuncSetAttribute(k_decode_attention_q4<Core>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, kQ4Smem<Core>);
     if (e == cudaSuccess)
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_decode_attention_q4, kQ4Threads,
-                                                        kQ4Smem);
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_decode_attention_q4<Core>,
+                                                        kQ4Threads, kQ4Smem<Core>);
     if (e != cudaSuccess || per_sm < 1) {
       *err = e != cudaSuccess ? e : cudaErrorInvalidConfiguration;
       return 0;
@@ -589,6 +818,15 @@ static int q4_grid(cudaError_t* err) {
     grid[dev] = sms * per_sm < kQ4MaxCtas ? sms * per_sm : kQ4MaxCtas;
   }
   return grid[dev];
+}
+
+template <class Core>
+static cudaError_t q4_launch(const AttnQ4Params& a, cudaStream_t stream) {
+  cudaError_t e = cudaSuccess;
+  const int grid = q4_grid<Core>(&e);
+  if (!grid) return e;
+  k_decode_attention_q4<Core><<<grid, kQ4Threads, kQ4Smem<Core>, stream>>>(a);
+  return cudaGetLastError();
 }
 
 static size_t q4_workspace(int nh, int nkv) {
@@ -662,14 +900,8 @@ ws_status ws_decode_attention_q4(const float *q, const float *k_new, const float
     set_error("device error flag unavailable");
     return WS_ERR_CUDA;
   }
-  cudaError_t e = cudaSuccess;
-  const int grid = q4_grid(&e);
-  if (!grid) {
-    set_error("4-bit decode attention setup failed: %s", cudaGetErrorString(e));
-    return WS_ERR_CUDA;
-  }
-  k_decode_attention_q4<<<grid, kQ4Threads, kQ4Smem, (cudaStream_t)stream>>>(a);
-  e = cudaGetLastError();
+  const cudaError_t e = a.G <= Q4Narrow::kHeads ? q4_launch<Q4Narrow>(a, (cudaStream_t)stream)
+                                                : q4_launch<Q4Wide>(a, (cudaStream_t)stream);
   if (e != cudaSuccess) {
     set_error("launch failed: %s", cudaGetErrorString(e));
     return WS_ERR_CUDA;
