@@ -81,6 +81,21 @@ __device__ __forceinline__ void q4_split(float a, float b, uint32_t& hi, uint32_
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
+// bf16 halves of a word in fp32 arithmetic by the mixed fma (one exact product,
+// one rounding): v + c x, x the low or the high half, c a bf16 twice in a word.
+__device__ __forceinline__ float q4_fma_low(uint32_t u, uint32_t c, float v) {
+  float r;
+  asm("{\n\t.reg .b16 l, h, o, p;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 {o, p}, %2;\n\t"
+      "fma.rn.f32.bf16 %0, l, o, %3;\n\t}" : "=f"(r) : "r"(u), "r"(c), "f"(v));
+  return r;
+}
+__device__ __forceinline__ float q4_fma_high(uint32_t u, uint32_t c, float v) {
+  float r;
+  asm("{\n\t.reg .b16 l, h, o, p;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 {o, p}, %2;\n\t"
+      "fma.rn.f32.bf16 %0, h, p, %3;\n\t}" : "=f"(r) : "r"(u), "r"(c), "f"(v));
+  return r;
+}
+
 __device__ __forceinline__ float q4_exp2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -457,7 +472,7 @@ struct Q4Narrow {
 
   __device__ __forceinline__ void tile(const unsigned char* st, int slot0, int pos, const Shared&) {
     const int lane = threadIdx.x & 31, rg = lane >> 2, rt = lane & 3;
-    const uint32_t zmask = rt < 2 ? 0xffffffffu : 0u;
+    const uint32_t zmask = rt < 2 ? 0xffffffffu : 0u, minus = rt < 2 ? 0x80008000u : 0xbf80bf80u;
     // scores: slots 16 u + 8 n + rg, heads 2 (rt & 1) + e
     float s[2][2][2];
 #pragma unroll
@@ -545,9 +560,13 @@ struct Q4Narrow {
         for (int n = 0; n < 2; ++n) {
           const uint32_t sz = reinterpret_cast<const uint32_t*>(&vs[n])[g];
           const float sc = bf16lo(sz), z = bf16hi(sz);
-          uint32_t hi, lo;
-          q4_split(s[u][n][0] * sc, s[u][n][1] * sc, hi, lo);
-          pb[n] = q4_transpose(rt < 2 ? hi : lo);
+          // hi terms in the lanes rt < 2; the others take them off first
+          const float p0 = s[u][n][0] * sc, p1 = s[u][n][1] * sc;
+          const __nv_bfloat162 hi = __floats2bfloat162_rn(p0, p1);
+          const uint32_t h = *reinterpret_cast<const uint32_t*>(&hi);
+          const __nv_bfloat162 part =
+              __floats2bfloat162_rn(q4_fma_low(h, minus, p0), q4_fma_high(h, minus, p1));
+          pb[n] = q4_transpose(*reinterpret_cast<const uint32_t*>(&part));
           zo[g][0] = fmaf(s[u][n][0], z, zo[g][0]);
           zo[g][1] = fmaf(s[u][n][1], z, zo[g][1]);
           const uint32_t w0 = g < 2 ? vw[n][0].x : vw[n][0].y, w1 = g < 2 ? vw[n][1].x : vw[n][1].y;
