@@ -239,21 +239,12 @@ struct LpShared {
   unsigned long long buf[kLpBuf];  // (not there without alternatives)
 };
 constexpr int kLpRing = kLpStages * kLpThreads * kLpBytes;
-static_assert(kLpRing >= kLpSplits * kMaxTop * 8, "the ring takes the splits' best");
 
-// The whole CTA: the 32 largest of the n keys at `from`, in falling order,
-// become the only candidates, and the threshold the k-th of them plus `plus`.
-__device__ __noinline__ void lp_compact(LpShared& sh, const unsigned long long* from, int n, int k,
-                                        int plus) {
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  unsigned long long mine = 0;
-  for (int i = warp * 32; i < n; i += kLpThreads) {
-    const unsigned long long key = i + lane < n ? from[i + lane] : 0;
-    if (__any_sync(0xffffffffu, key > __shfl_sync(0xffffffffu, mine, k - 1)))
-      mine = lp_merge(mine, lp_sort(key, lane), lane);
-  }
-  // the warps' lists in pairs; those past the candidates are empty
-  const int lists = min(kLpWarps, (n + 31) / 32);
+// The whole CTA: the 32 largest keys of the warps' lists (`mine`, in falling
+// order; those of the first `lists` warps are not empty) become the only
+// candidates, in falling order, and the threshold the k-th of them plus 1.
+__device__ __forceinline__ void lp_gather(LpShared& sh, unsigned long long mine, int lists, int k) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll 1
   for (int o = 1; o < lists; o <<= 1) {
     if ((warp & (2 * o - 1)) == o) sh.list[warp][lane] = mine;
@@ -263,16 +254,29 @@ __device__ __noinline__ void lp_compact(LpShared& sh, const unsigned long long* 
   __syncthreads();
   if (warp == 0) {
     sh.buf[lane] = mine;
-    if (lane == k - 1) sh.thr = mine ? mine + plus : 0;
+    if (lane == k - 1) sh.thr = mine ? mine + 1 : 0;
     const int have = __popc(__ballot_sync(0xffffffffu, mine != 0));
     if (lane == 0) sh.n = have;
   }
   __syncthreads();
 }
 
-// One CTA per (split, row).  DRAM bound: a ring of four steps of 8 KB in shared
-// memory, filled by bulk copies, three of them under way while one is worked
-// on; registers hold one step only.  The best `k` are found in the same pass:
+// The same of the n candidates so far.
+__device__ __noinline__ void lp_compact(LpShared& sh, int n, int k) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  unsigned long long mine = 0;
+  for (int i = warp * 32; i < n; i += kLpThreads) {
+    const unsigned long long key = i + lane < n ? sh.buf[i + lane] : 0;
+    if (__any_sync(0xffffffffu, key > __shfl_sync(0xffffffffu, mine, k - 1)))
+      mine = lp_merge(mine, lp_sort(key, lane), lane);
+  }
+  lp_gather(sh, mine, min(kLpWarps, (n + 31) / 32), k);
+}
+
+// One CTA per (split, row).  A ring of two steps of 8 KB in shared memory filled
+// by bulk copies, so that registers hold one step and eight CTAs share a SM
+// (three steps and fewer CTAs were slower: the steps' barrier is what costs, and
+// the other CTAs cover it).  The best `k` are found in the same pass:
 // the k-th of the threads' largest values of the first step bounds the k-th of
 // all from below, so that only the few values from there on become candidates;
 // their best ones raise the bound when there are many, which an order that
@@ -310,6 +314,10 @@ __global__ void __launch_bounds__(kLpThreads, 8) k_token_logprobs(const __grid_c
     for (int i = 0; i < kLpStages && i < steps; ++i) fill(i);
   }
   __syncthreads();
+
+  // the target's logit, in time for the end
+  const int target = t == 0 && a.targets ? a.targets[r] : -1;
+  const float target_x = target >= 0 && target < a.V ? lp_value<DT>(row, target) : 0.f;
 
   LpSum s = {-FLT_MAX, 0.f, 0.f};
   unsigned long long thr = 0;
@@ -412,7 +420,7 @@ __global__ void __launch_bounds__(kLpThreads, 8) k_token_logprobs(const __grid_c
         if (TOP) {
           const int n = sh.n;
           again = n > kLpBuf;
-          lp_compact(sh, sh.buf, min(n, kLpBuf), a.k, 1);
+          lp_compact(sh, min(n, kLpBuf), a.k);
           thr = sh.thr;
           thrv = thr >> 32 ? key_value(thr) : -INFINITY;
           over = 0;
@@ -427,7 +435,7 @@ __global__ void __launch_bounds__(kLpThreads, 8) k_token_logprobs(const __grid_c
   }
   if (TOP) {
     __syncthreads();
-    lp_compact(sh, sh.buf, sh.n, a.k, 1);
+    lp_compact(sh, sh.n, a.k);
   }
   s.join_lanes(32);
   if (lane == 0) sh.sums[warp] = s;
@@ -461,12 +469,26 @@ __global__ void __launch_bounds__(kLpThreads, 8) k_token_logprobs(const __grid_c
       s.join_lanes(32);
     }
     if (TOP) {
+      // lists in falling order already, four on their way at a time; short ones
+      // are sorted again, 32 keys at once (a sort and a merge take as long as
+      // four merges)
+      unsigned long long mine = 0;
       const int n = a.splits * a.k;
-      // (the ring's copies are all done and read)
-      unsigned long long* all = reinterpret_cast<unsigned long long*>(smem);
-      for (int i = t; i < n; i += kLpThreads) all[i] = __ldcg(a.keys + at * a.k + i);
-      __syncthreads();
-      lp_compact(sh, all, n, a.k, 1);
+      if (a.k <= 8)
+        for (int i = warp * 32; i < n; i += kLpThreads)
+          mine = lp_merge(mine, lp_sort(i + lane < n ? __ldcg(a.keys + at * a.k + i + lane) : 0ull, lane), lane);
+      else
+        for (int i0 = warp; i0 < a.splits; i0 += 4 * kLpWarps) {
+          unsigned long long key[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * kLpWarps;
+            key[u] = i < a.splits && lane < a.k ? __ldcg(a.keys + (at + i) * a.k + lane) : 0;
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mine = lp_merge(mine, key[u], lane);
+        }
+      lp_gather(sh, mine, min(kLpWarps, a.k <= 8 ? (n + 31) / 32 : a.splits), a.k);
     }
   }
   if (warp > 0) return;
@@ -475,13 +497,12 @@ __global__ void __launch_bounds__(kLpThreads, 8) k_token_logprobs(const __grid_c
   if (t == 0) {
     if (a.entropy) a.entropy[r] = lz - s.t / s.z / kLog2e;
     if (a.targets) {
-      const int i = a.targets[r];
       float lp = 0.f;
-      if (i >= a.V) {
+      if (target >= a.V) {
         atomicExch(a.err, kDerrBadToken);
         lp = NAN;
-      } else if (i >= 0) {
-        lp = lp_value<DT>(row, i) - s.m - lz;
+      } else if (target >= 0) {
+        lp = target_x - s.m - lz;
       }
       a.logprob[r] = lp;
     }
