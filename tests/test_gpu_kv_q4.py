@@ -132,6 +132,33 @@ def test_special_values():
     assert np.array_equal(kb.cpu().numpy(), sv.dequantize_rows(sz, True), equal_nan=True)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_codes_next_to_ties_and_of_every_size(dtype):
+    """Groups whose values lie on, next to and between the ties of their own
+    steps, at sizes from the subnormals up: the codes are those of the division."""
+    r = np.random.default_rng(11)
+    T = 3000
+    top = 2.0 ** r.integers(*((-13, 15) if dtype == torch.float16 else (-133, 124)), (T, 1, 1))
+    x = r.standard_normal((T, 4, 32)) * top
+    n = r.integers(0, 30, (T, 4, 32)) / 2.0
+    lo, hi = x.min(-1, keepdims=True), x.max(-1, keepdims=True)
+    on = lo + n * ((hi - lo) / 15)                    # a multiple of half a step from the least
+    x = np.where(r.random(x.shape) < 0.7, on, x)
+    s = torch.from_numpy(((hi - lo) / 15).astype(np.float32)).bfloat16().float().numpy()
+    z = torch.from_numpy((lo + 8 * s).astype(np.float32)).bfloat16().float().numpy()
+    tie = (z + (n - 8.5) * s).astype(np.float32)      # on the ties of the step as it is stored
+    x = np.where(r.random(x.shape) < 0.4, tie, x)
+    k = torch.from_numpy(x.reshape(T, 1, D)).float().to(dtype)
+    kc = torch.zeros((T, 1, 1, 80), dtype=torch.uint8, device="cuda")
+    vc = kc.clone()
+    wb.kv_store_q4(k.cuda(), k.cuda(), kc, vc, _i32([0] * T))
+    torch.cuda.synchronize()
+    for c, keys in ((kc, True), (vc, False)):
+        ref = sv.quantize_rows(k.float().numpy(), keys)
+        bad = (c.cpu().numpy()[:, :, 0] != ref).any(-1)
+        assert not bad.any(), f"{bad.sum()} rows differ, first {np.argwhere(bad)[0]}"
+
+
 def test_strided_rows_of_a_fused_projection():
     T, nkv = 19, 2
     k, v = _kv(T, nkv, torch.bfloat16, 4)

@@ -89,7 +89,7 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 // fp32: s = bf16((max - min) / 15), taken as 0 below 2^-126; z = bf16(min +
 // 8 s); q = clamp(rint((x - z) / s) + 8, 0, 15), 8 where s is 0.  A group
 // with a value that is not finite stands for NaN as a whole.
-__device__ __forceinline__ uint32_t quantize8(const float (&x)[8], uint32_t& sz) {
+__device__ __forceinline__ uint32_t quantize8(float (&x)[8], uint32_t& sz) {
   float lo = min_nan(min3_nan(x[0], x[1], x[2]), min3_nan(x[3], x[4], x[5]));
   float hi = max_nan(max3_nan(x[0], x[1], x[2]), max3_nan(x[3], x[4], x[5]));
   lo = min3_nan(lo, x[6], x[7]);
@@ -99,40 +99,42 @@ __device__ __forceinline__ uint32_t quantize8(const float (&x)[8], uint32_t& sz)
     lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
-  const float s32 = __fdiv_rn(__fsub_rn(hi, lo), 15.f);
+  // (max - min) / 15, corrected once by its exact remainder (Markstein's
+  // quotient: with the rounded reciprocal that is the rounded quotient)
+  const float range = __fsub_rn(hi, lo), y = 1.f / 15.f, s0 = __fmul_rn(range, y);
+  const float s32 = __fmaf_rn(__fmaf_rn(-s0, 15.f, range), y, s0);
   if (!(s32 <= FLT_MAX)) {  // a NaN or an infinity in the group
     sz = kBf16Nan | (kBf16Nan << 16);
     return 0x88888888u;
   }
   float s = __bfloat162float(__float2bfloat16_rn(s32));
   if (s < 1.17549435e-38f) s = 0.f;
-  const float z = __bfloat162float(__float2bfloat16_rn(__fadd_rn(lo, 8.f * s)));
+  float z = __bfloat162float(__float2bfloat16_rn(__fadd_rn(lo, 8.f * s)));
   sz = (__float_as_uint(s) >> 16) | (__float_as_uint(z) & 0xffff0000u);
   if (s == 0.f) return 0x88888888u;
-  // n = rint(d / s), d = x - z: rounded from the product with an approximate
-  // 1 / s, then held against the exact remainder d - n s (n s has 12 bits), which
-  // is at most s / 2, and s / 2 only for an even n.  (The rounded quotient is a
-  // tie only where d / s is one: d next to (n + 1/2) s is at least 2^-24 of it
-  // away, more than half a unit of n + 1/2.)  Adding 1.5 2^23 + 8 rounds to even
-  // and leaves n + 8 in the low bits.
+  if (s < 0x1p-90f) {  // away from the subnormals, where the remainder would be rounded
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] *= 0x1p64f;
+    z *= 0x1p64f;
+    s *= 0x1p64f;
+  }
+  // rint(d / s), d = x - z: d times an approximate 1 / s, corrected by the exact
+  // remainder.  That is within 2^-45 of d / s before it is rounded, so a tie
+  // comes out as one, and nothing else does: d next to (n + 1/2) s, which has 12
+  // bits, is more than (1 + 2^-12) 2^-24 of it away, half a unit of n + 1/2 at
+  // most 2^-24.  Adding 1.5 2^23 + 8 rounds to even and leaves rint + 8 in the
+  // low bits.
   constexpr float kMagic = 12582912.f;
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-  const float half = 0.5f * s;
-  float c[8], rem[8];
-  bool near = false;
+  float c[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float d = __fsub_rn(x[i], z);
-    c[i] = __fmaf_rn(d, r, kMagic + 8.f);
-    rem[i] = __fmaf_rn(__fsub_rn(kMagic + 8.f, c[i]), s, d);
-    near |= fabsf(rem[i]) >= half;
-  }
-  if (near) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (fabsf(rem[i]) > half || (fabsf(rem[i]) == half && (__float_as_uint(c[i]) & 1u)))
-        c[i] += copysignf(1.f, rem[i]);
+  for (int i = 0; i < 8; i += 2) {
+    const float2 d = add2(make_float2(x[i], x[i + 1]), make_float2(-z, -z)), rr = make_float2(r, r);
+    const float2 q = mul2(d, rr), e = fma2(q, make_float2(-s, -s), d);
+    const float2 n = add2(fma2(e, rr, q), make_float2(kMagic + 8.f, kMagic + 8.f));
+    c[i] = n.x;
+    c[i + 1] = n.y;
   }
   // two codes at a time, clamped to 4 bits, above the ones before them
   uint32_t w = 0;
