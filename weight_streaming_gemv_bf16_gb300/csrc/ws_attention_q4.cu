@@ -620,6 +620,8 @@ __global__ void __launch_bounds__(kQ4Threads, Core::kCtas)
   __shared__ int last;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, G = a.G;
 
+  pdl_launch_dependents();
+  pdl_wait();
   // the tiles of all rows and heads, cut into as many equal runs as there are
   // CTAs; every warp finds the run's place by itself
   // (fewer than 2^31 of them: a tile is 5120 bytes of cache)
@@ -844,8 +846,8 @@ static cudaError_t q4_launch(const AttnQ4Params& a, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   const int grid = q4_grid<Core>(&e);
   if (!grid) return e;
-  k_decode_attention_q4<Core><<<grid, kQ4Threads, kQ4Smem<Core>, stream>>>(a);
-  return cudaGetLastError();
+  e = launch_serving(k_decode_attention_q4<Core>, dim3(grid), kQ4Threads, kQ4Smem<Core>, stream, a);
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 static size_t q4_workspace(int nh, int nkv) {

@@ -70,6 +70,8 @@ constexpr int kKvBatch = 4;  // tokens whose loads a warp has in flight together
 // A warp takes `per` tokens of one head, kKvWarps apart.
 template <int DT>
 __global__ void __launch_bounds__(kKvWarps * 32, 4) k_kv_store_q4(const __grid_constant__ KvRowsParams a) {
+  pdl_launch_dependents();
+  pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = blockIdx.y;
   const int base = blockIdx.x * kKvWarps * a.per + warp;
   const bool keys = lane < 16;
@@ -108,6 +110,8 @@ __global__ void __launch_bounds__(kKvWarps * 32, 4) k_kv_store_q4(const __grid_c
 
 template <int DT>
 __global__ void __launch_bounds__(kKvWarps * 32) k_kv_load_q4(const __grid_constant__ KvRowsParams a) {
+  pdl_launch_dependents();
+  pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = blockIdx.y;
   const int base = blockIdx.x * kKvWarps * a.per + warp;
   const bool keys = lane < 16;
@@ -174,16 +178,17 @@ static ws_status kv_rows(KvRowsParams& a, int dtype, int head_dim, bool store,
   // search for a token's sequence is made once and four loads are in flight
   a.per = (long long)a.T * a.nkv > 16 * 1024 ? 8 : 1;
   const dim3 grid((a.T + kKvWarps * a.per - 1) / (kKvWarps * a.per), a.nkv);
+  cudaError_t e;
   if (store) {
-    if (dtype == WS_DTYPE_F32) k_kv_store_q4<DT_F32><<<grid, kKvWarps * 32, 0, stream>>>(a);
-    else if (dtype == WS_DTYPE_BF16) k_kv_store_q4<DT_BF16><<<grid, kKvWarps * 32, 0, stream>>>(a);
-    else k_kv_store_q4<DT_F16><<<grid, kKvWarps * 32, 0, stream>>>(a);
+    if (dtype == WS_DTYPE_F32) e = launch_serving(k_kv_store_q4<DT_F32>, grid, kKvWarps * 32, 0, stream, a);
+    else if (dtype == WS_DTYPE_BF16) e = launch_serving(k_kv_store_q4<DT_BF16>, grid, kKvWarps * 32, 0, stream, a);
+    else e = launch_serving(k_kv_store_q4<DT_F16>, grid, kKvWarps * 32, 0, stream, a);
   } else {
-    if (dtype == WS_DTYPE_F32) k_kv_load_q4<DT_F32><<<grid, kKvWarps * 32, 0, stream>>>(a);
-    else if (dtype == WS_DTYPE_BF16) k_kv_load_q4<DT_BF16><<<grid, kKvWarps * 32, 0, stream>>>(a);
-    else k_kv_load_q4<DT_F16><<<grid, kKvWarps * 32, 0, stream>>>(a);
+    if (dtype == WS_DTYPE_F32) e = launch_serving(k_kv_load_q4<DT_F32>, grid, kKvWarps * 32, 0, stream, a);
+    else if (dtype == WS_DTYPE_BF16) e = launch_serving(k_kv_load_q4<DT_BF16>, grid, kKvWarps * 32, 0, stream, a);
+    else e = launch_serving(k_kv_load_q4<DT_F16>, grid, kKvWarps * 32, 0, stream, a);
   }
-  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("launch failed: %s", cudaGetErrorString(e));
     return WS_ERR_CUDA;

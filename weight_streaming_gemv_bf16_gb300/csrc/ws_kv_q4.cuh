@@ -30,6 +30,26 @@
 
 namespace ws {
 
+// A launch that may begin while the kernel before it on the stream drains: its
+// setup (barriers, tensor memory, its place in the grid) overlaps that kernel's
+// last CTAs.  The kernels launched so wait for everything before them
+// (pdl_wait) ahead of their first access to memory, in every thread.
+template <typename P>
+inline cudaError_t launch_serving(void (*kernel)(const P), dim3 grid, int threads, int smem,
+                                  cudaStream_t stream, const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 constexpr int kKvDim = 128;
 constexpr int kKvGroup = 32;
 constexpr int kKvCodes = kKvDim / 2;                              // bytes of codes

@@ -311,6 +311,10 @@ __global__ void __launch_bounds__(kLpThreads, 8) k_token_logprobs(const __grid_c
     fence_mbar_init();
     sh.n = 0;
     sh.abort = 0;
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+  if (t == 0) {
     for (int i = 0; i < kLpStages && i < steps; ++i) fill(i);
   }
   __syncthreads();
@@ -629,16 +633,16 @@ ws_status ws_token_logprobs(const void *logits, int dtype, long long ld, const i
   const int grid = rows * a.splits;
   const int sm = topk ? kLpSmemTop : kLpSmem;
   if (dtype == WS_DTYPE_F32) {
-    if (topk) k_token_logprobs<DT_F32, true><<<grid, kLpThreads, sm, st>>>(a);
-    else k_token_logprobs<DT_F32, false><<<grid, kLpThreads, sm, st>>>(a);
+    if (topk) e = launch_serving(k_token_logprobs<DT_F32, true>, dim3(grid), kLpThreads, sm, st, a);
+    else e = launch_serving(k_token_logprobs<DT_F32, false>, dim3(grid), kLpThreads, sm, st, a);
   } else if (dtype == WS_DTYPE_BF16) {
-    if (topk) k_token_logprobs<DT_BF16, true><<<grid, kLpThreads, sm, st>>>(a);
-    else k_token_logprobs<DT_BF16, false><<<grid, kLpThreads, sm, st>>>(a);
+    if (topk) e = launch_serving(k_token_logprobs<DT_BF16, true>, dim3(grid), kLpThreads, sm, st, a);
+    else e = launch_serving(k_token_logprobs<DT_BF16, false>, dim3(grid), kLpThreads, sm, st, a);
   } else {
-    if (topk) k_token_logprobs<DT_F16, true><<<grid, kLpThreads, sm, st>>>(a);
-    else k_token_logprobs<DT_F16, false><<<grid, kLpThreads, sm, st>>>(a);
+    if (topk) e = launch_serving(k_token_logprobs<DT_F16, true>, dim3(grid), kLpThreads, sm, st, a);
+    else e = launch_serving(k_token_logprobs<DT_F16, false>, dim3(grid), kLpThreads, sm, st, a);
   }
-  e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("launch failed: %s", cudaGetErrorString(e));
     return WS_ERR_CUDA;

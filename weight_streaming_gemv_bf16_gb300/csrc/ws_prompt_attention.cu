@@ -205,6 +205,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   __shared__ PaShared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 10 && lane < 3) tma_prefetch_map(lane == 0 ? &a.mq : lane == 1 ? &a.mk : &a.mv);
+  pdl_launch_dependents();
+  pdl_wait();
   const int heads = a.pair ? a.nh / 2 : a.nh, rows = a.pair ? kPaTile : 2 * kPaTile;
   int first, len, block;
   if (!pa_place(a, blockIdx.x / heads, rows, first, len, block)) return;
@@ -628,10 +630,10 @@ ws_status ws_prompt_attention(const void *q, const void *k, const void *v, int d
     return WS_ERR_CUDA;
   }
   if (dtype == WS_DTYPE_F16)
-    k_prompt_attention<DT_F16><<<(int)grid, kPaThreads, kPaSmem, (cudaStream_t)stream>>>(a);
+    e = launch_serving(k_prompt_attention<DT_F16>, dim3((unsigned)grid), kPaThreads, kPaSmem, (cudaStream_t)stream, a);
   else
-    k_prompt_attention<DT_BF16><<<(int)grid, kPaThreads, kPaSmem, (cudaStream_t)stream>>>(a);
-  e = cudaGetLastError();
+    e = launch_serving(k_prompt_attention<DT_BF16>, dim3((unsigned)grid), kPaThreads, kPaSmem, (cudaStream_t)stream, a);
+  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("launch failed: %s", cudaGetErrorString(e));
     return WS_ERR_CUDA;
