@@ -213,7 +213,12 @@ ws_status ws_decode_attention(const float *q, const float *k_new, const float *v
                               int s_max, void *workspace, size_t workspace_bytes,
                               ws_stream_t stream);
 
-/* Causal attention over packed prompts: token t of a sequence attends to that
+/* The serving operators from here to ws_token_logprobs launch one kernel each,
+ * which may begin its setup while the kernel before it on the stream drains and
+ * waits for that kernel ahead of its first access to memory.  The first call of
+ * each on a device sets its kernels up: make it before any stream capture.
+ *
+ * Causal attention over packed prompts: token t of a sequence attends to that
  * sequence's tokens up to and including t.  Query head h reads key-value head
  * h / (n_heads / n_kv_heads) with scores q.k / sqrt(128) and an fp32 softmax.
  * q [T][n_heads][128], k and v [T][n_kv_heads][128], bf16 or fp16 (dtype), a
@@ -262,7 +267,8 @@ ws_status ws_prompt_attention(const void *q, const void *k, const void *v, int d
  * ws_kv_load_q4: the reverse, with the same arguments: the values that the
  * rows stand for, rounded once to dtype, to k and v contiguous [T][n_kv_heads]
  * [128]; skipped tokens are left as they were.
- * head_dim must be 128, n_kv_heads at most 65535, strides a multiple of 8,
+ * head_dim must be 128, n_kv_heads at most 65535, T at most 2^30, strides a
+ * multiple of 8,
  * every matrix 16-byte aligned.  ws_kv_q4_row_bytes: 80, or 0 for another
  * head_dim. */
 size_t ws_kv_q4_row_bytes(int head_dim);
@@ -297,8 +303,8 @@ ws_status ws_decode_attention_q4(const float *q, const float *k_new, const float
                                  int s_max, void *workspace, size_t workspace_bytes,
                                  ws_stream_t stream);
 
-/* Log-probabilities over rows of logits (fp32, bf16 or fp16; V values a row,
- * rows ld >= V elements apart; the ones behind V are not read).  With
+/* Log-probabilities over rows of logits (fp32, bf16 or fp16; V values a row, at
+ * most 2^28, rows ld >= V elements apart; the ones behind V are not read).  With
  * p = softmax of the row, everything natural and in fp32:
  *  - logprob[r] = log p[targets[r]] (both int32 / fp32 [rows], or both NULL);
  *    0 where the target is negative (no token), NaN and the device error flag

@@ -92,9 +92,9 @@ def _softmax_rows(s, v):
 
 def decode_attention_q4(q, k_new, v_new, k_cache, v_cache, pos):
     """q [B, nh * 128], new rows [B, nkv * 128] fp32, caches uint8 [B, nkv, S,
-    80].  Returns out and its absolute sum (sum_j p_j |v_j|) [B, nh * 128], the
-    largest sum_d |q_d k_d| / sqrt(d) per row and head [B, nh], and the updated
-    caches; rows with a position outside 0 .. S - 1 are left out (NaN)."""
+    80].  Returns out and the absolute sum of its parts (sum_j p_j (|s_j (q_j -
+    8)| + |z_j|)) [B, nh * 128], the largest sum_d |q_d| (|s (code - 8)| + |z|) /
+    sqrt(d) over the slots per row and head [B, nh], and the updated caches; rows with a position outside 0 .. S - 1 are left out (NaN)."""
     B, nkv, S, _ = k_cache.shape
     nh = q.shape[1] // D
     kc, vc = k_cache.copy(), v_cache.copy()
@@ -110,13 +110,14 @@ def decode_attention_q4(q, k_new, v_new, k_cache, v_cache, pos):
         for h in range(nh):
             g = h // (nh // nkv)
             c, s, z = (x.astype(np.float64) for x in row_values(kc[b, g, :p + 1], True))
-            K = s * c + z
+            K, Ka = s * c + z, np.abs(s * c) + np.abs(z)
             c, s, z = (x.astype(np.float64) for x in row_values(vc[b, g, :p + 1], False))
-            V = s * c + z
+            V, Va = s * c + z, np.abs(s * c) + np.abs(z)
             qh = np.asarray(q[b, h * D:(h + 1) * D], np.float64)
-            o, _, a = _softmax_rows((K @ qh)[None] / np.sqrt(D), V)
-            out[b, h * D:(h + 1) * D], mag[b, h * D:(h + 1) * D] = o[0], a[0]
-            top[b, h] = (np.abs(K) @ np.abs(qh)).max() / np.sqrt(D)
+            o, _, a = _softmax_rows((K @ qh)[None] / np.sqrt(D), np.concatenate([V, Va], axis=1))
+            out[b, h * D:(h + 1) * D], mag[b, h * D:(h + 1) * D] = o[0, :D], a[0, D:]
+            with np.errstate(all="ignore"):
+                top[b, h] = (Ka @ np.abs(qh)).max() / np.sqrt(D)
     return out, mag, top, kc, vc
 
 

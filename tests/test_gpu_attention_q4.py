@@ -1,12 +1,15 @@
 """GPU parity of the decode attention over the 4-bit cache against the double
 oracle on the same bytes.
 
-Tolerance (fp32 output).  q enters as a bf16 pair (2^-17 of each element), so a
-score is off by at most 2^-17 of sum |q k| / sqrt(128) = `top`, and by the fp32
-sums of 128 products, 128 2^-24 of it: together under 2^-16 top.  That moves a
-probability by 2^-16 top relative, twice (numerator and sum); the probability
-pair adds 2^-17, exp2 and the sums a few 2^-22: |error| <= mag (2^-15 top +
-2^-15), mag = sum p |v|.  The bf16 output is the fp32 one rounded."""
+Tolerance (fp32 output).  A score is sum_g s_g (sum q (code - 8)) + z_g (sum
+q): q enters as a bf16 pair (2^-17 of each element) in both, so it is off by at
+most 2^-17 of `top` = sum |q| (|s (code - 8)| + |z|) / sqrt(128), and by the
+fp32 sums of 128 and 4 terms, 132 2^-24 of it: together under 2^-16 top.  That
+moves a probability by 2^-16 top relative, twice (numerator and sum).  The
+values enter as s (code - 8) and z apart, each times a probability: the pair adds
+2^-17 of either part, exp2, the sums and the merges a few 2^-22: |error| <= mag
+(2^-15 top + 2^-15), mag = sum p (|s (code - 8)| + |z|).  The bf16 output is the
+fp32 one rounded."""
 import numpy as np
 import pytest
 import torch
@@ -192,6 +195,72 @@ def test_runs_are_bit_identical():
         outs.append(o)
     torch.cuda.synchronize()
     assert all(torch.equal(o, outs[0]) for o in outs[1:])
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Each with a workspace of its own, long enough to overlap; replayed from
+    two graphs too."""
+    hosts = [_inputs(2, 12, 2, 6000, [5999, 3000], 31), _inputs(3, 8, 8, 2500, [2499, 1200, 7], 32)]
+    pos = [[5999, 3000], [2499, 1200, 7]]
+    dev = [_dev(*h) for h in hosts]
+    ps = [torch.tensor(p, dtype=torch.int32, device="cuda") for p in pos]
+    wss = [_ws(2, 12, 2, 6000), _ws(3, 8, 8, 2500)]
+    outs = [torch.full((d[0].shape[0], d[0].shape[1]), 7.0, device="cuda") for d in dev]
+    streams = [torch.cuda.Stream() for _ in dev]
+    torch.cuda.synchronize()
+    def call(i, stream=None):
+        wb.decode_attention_q4(*dev[i], ps[i], wss[i], out_f32=outs[i], stream=stream)
+    for _ in range(5):
+        for i in range(2):
+            call(i, streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        _compare(*hosts[i], pos[i], outs[i], None, dev[i][3], dev[i][4])
+        outs[i].fill_(7.0)
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=streams[i]):
+            call(i)
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        _compare(*hosts[i], pos[i], outs[i], None, dev[i][3], dev[i][4])
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-6, 1e6, 1e18])
+def test_values_of_every_size(size):
+    """Values far from one, down to steps near the smallest normals of bf16."""
+    host = list(_inputs(2, 6, 2, 200, [199, 30], 15))
+    r = np.random.default_rng(15)
+    for b, p in enumerate([199, 30]):
+        host[4][b, :, :p] = sv.quantize_rows((r.standard_normal((2, p, D)) * size).astype(np.float32), False)
+    host[2] = (host[2] * size).astype(np.float32)
+    q, kn, vn, kc, vc = _dev(*host)
+    o = torch.full((2, 6 * D), 7.0, device="cuda")
+    p = torch.tensor([199, 30], dtype=torch.int32, device="cuda")
+    wb.decode_attention_q4(q, kn, vn, kc, vc, p, _ws(2, 6, 2, 200), out_f32=o)
+    torch.cuda.synchronize()
+    _compare(*host, [199, 30], o, None, kc, vc)
+
+
+@pytest.mark.parametrize("nh", [2, 6])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_queries_that_are_not_finite(nh, bad):
+    """One head's query: NaN for that head alone."""
+    host = list(_inputs(1, nh, 1, 100, [80], 16))
+    host[0][0, D + 5] = bad
+    q, kn, vn, kc, vc = _dev(*host)
+    o = torch.zeros((1, nh * D), device="cuda")
+    p = torch.tensor([80], dtype=torch.int32, device="cuda")
+    wb.decode_attention_q4(q, kn, vn, kc, vc, p, _ws(1, nh, 1, 100), out_f32=o)
+    nan = torch.isnan(o).cpu().view(nh, D)
+    assert nan[1].all() and not nan[0].any() and not nan[2:].any()
 
 
 def test_appends_the_bytes_that_the_store_writes():

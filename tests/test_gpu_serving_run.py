@@ -79,3 +79,54 @@ def test_prompts_cache_decode_and_answers():
         dpos += (dpos >= 0).int()
         pos = dpos.cpu().numpy()
     assert wb.device_error(reset=True) == 0
+
+
+def test_calls_that_feed_one_another():
+    """Each call reads what the one before it wrote, with nothing in between but
+    the stream's order; the same calls with a synchronisation after each give
+    the same bits."""
+    import __graft_entry__
+    __graft_entry__.build()
+    torch.cuda.set_device(0)
+    g = torch.Generator().manual_seed(3)
+    T, nh, nkv, S, V = 300, 4, 2, 400, 5000
+    q0 = torch.randn(T, nh, D, generator=g).bfloat16().cuda()
+    kv = torch.randn(T, 2 * nkv, D, generator=g).bfloat16().cuda()
+    cu = torch.tensor([0, 170, 300], dtype=torch.int32, device="cuda")
+    start = torch.zeros(2, dtype=torch.int32, device="cuda")
+    dec = torch.randn(2, nh * D, generator=g).cuda()
+    new = torch.randn(2, nkv * D, generator=g).cuda()
+    head = torch.randn(V, nh * D, generator=g).cuda()
+    lws = torch.zeros(wb.logprobs_workspace_bytes(2, V, 4), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(wb.attention_q4_workspace_bytes(2, nh, nkv, S), dtype=torch.uint8, device="cuda")
+
+    def program(sync):
+        done = torch.cuda.synchronize if sync else (lambda: None)
+        a, b = torch.zeros_like(q0).view(T, nh * D), torch.zeros_like(q0).view(T, nh * D)
+        kc, vc = wb.new_kv_cache_q4(2, nkv, S), wb.new_kv_cache_q4(2, nkv, S)
+        kb, vb = torch.zeros(T, nkv, D, device="cuda").bfloat16(), torch.zeros(T, nkv, D, device="cuda").bfloat16()
+        q, k, v = q0, kv[:, :nkv], kv[:, nkv:]
+        o, prev = torch.zeros_like(dec), dec
+        ent = torch.zeros(2, device="cuda")
+        top = torch.zeros((2, 4), dtype=torch.int32, device="cuda")
+        pos = torch.tensor([170, 130], dtype=torch.int32, device="cuda")
+        seen = []
+        for i in range(6):
+            out = a if i % 2 == 0 else b
+            wb.prompt_attention(q, k, v, cu, out); done()
+            wb.kv_store_q4(k, out.view(T, nh, D)[:, :nkv], kc, vc, start, cu_seqlens=cu); done()
+            wb.kv_load_q4(kc, vc, start, kb, vb, cu_seqlens=cu); done()
+            q, k, v = out.view(T, nh, D), kb, vb
+            wb.decode_attention_q4(prev, new, new, kc, vc, pos, ws, out_f32=o); done()
+            logits = o @ head.t(); done()
+            wb.token_logprobs(logits, lws, entropy=ent, top_idx=top); done()
+            prev = o.clone() * ent[:, None].clamp(0.5, 2.0); done()
+            seen += [out.clone(), kb.clone(), o.clone(), ent.clone(), top.clone()]
+            done()
+        torch.cuda.synchronize()
+        return seen
+
+    once = program(True)
+    for _ in range(3):
+        assert all(torch.equal(x, y) for x, y in zip(once, program(False)))
+    assert wb.device_error(reset=True) == 0

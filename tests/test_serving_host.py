@@ -49,7 +49,7 @@ STORE = dict(k=A, v=A, dtype=1, cu=A, rows=None, start=A, kc=A, vc=A, T=64, n=2,
     (dict(k=None), -1), (dict(v=None), -1), (dict(start=None), -1), (dict(kc=None), -1),
     (dict(vc=None), -1), (dict(dtype=7), -1), (dict(T=0), -3), (dict(n=0), -3),
     (dict(n_rows=0), -3), (dict(nkv=0), -3), (dict(nkv=65536), -3), (dict(S=0), -3),
-    (dict(d=64), -3), (dict(cu=None), -3), (dict(kc=MIS), -2), (dict(vc=MIS), -2),
+    (dict(d=64), -3), (dict(cu=None), -3), (dict(T=(1 << 30) + 1), -3), (dict(kc=MIS), -2), (dict(vc=MIS), -2),
     (dict(k=MIS), -2), (dict(v=MIS), -2),
 ])
 def test_kv_store_and_load_refusals(lib, change, status):
@@ -107,7 +107,7 @@ LOGP = dict(x=A, dtype=0, ld=100, tgt=A, lp=A, ent=A, ti=A, tl=A, rows=2, V=100,
     (dict(x=None), -1), (dict(ws=None), -1), (dict(tgt=None), -1), (dict(lp=None), -1),
     (dict(ti=None, tl=None), -1), (dict(tgt=None, lp=None, ent=None, k=0), -1),
     (dict(dtype=9), -1), (dict(wsb=16), -1), (dict(rows=0), -3), (dict(V=0), -3),
-    (dict(ld=99), -3), (dict(k=-1), -3), (dict(k=33), -3), (dict(V=4, k=5), -3),
+    (dict(ld=99), -3), (dict(V=(1 << 28) + 1, ld=1 << 30), -3), (dict(k=-1), -3), (dict(k=33), -3), (dict(V=4, k=5), -3),
     (dict(x=A + 2), -2), (dict(dtype=1, x=A + 1), -2), (dict(ws=MIS), -2),
 ])
 def test_token_logprobs_refusals(lib, change, status):

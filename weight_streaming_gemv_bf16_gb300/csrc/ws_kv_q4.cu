@@ -156,11 +156,11 @@ static ws_status kv_rows(KvRowsParams& a, int dtype, int head_dim, bool store,
     set_error("dtype must be WS_DTYPE_F32, WS_DTYPE_BF16 or WS_DTYPE_F16");
     return WS_ERR_ARG;
   }
-  if (a.T < 1 || a.n < 1 || a.n_rows < 1 || a.nkv < 1 || a.nkv > 65535 || a.S < 1 ||
+  if (a.T < 1 || a.T > (1 << 30) || a.n < 1 || a.n_rows < 1 || a.nkv < 1 || a.nkv > 65535 || a.S < 1 ||
       head_dim != kKvDim || (!a.cu && a.T != a.n) ||
       (store && (a.ks < (long long)a.nkv * kKvDim || a.vs < (long long)a.nkv * kKvDim ||
                  a.ks % 8 || a.vs % 8))) {
-    set_error("4-bit rows: T, sequences, rows, key-value heads (to 65535) and s_max at least 1, "
+    set_error("4-bit rows: T (to 2^30), sequences, rows, key-value heads (to 65535) and s_max at least 1, "
               "head_dim %d, T = sequences without bounds, token strides a multiple of 8 and at "
               "least n_kv_heads * %d", kKvDim, kKvDim);
     return WS_ERR_SHAPE;

@@ -14,6 +14,7 @@
 namespace ws {
 
 constexpr int kMaxTop = 32;         // alternatives a row: one a lane
+constexpr int kMaxVocab = 1 << 28;  // a row's bytes fit 32 bits
 constexpr int kLpThreads = 128;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpBytes = 64;        // of values that a thread takes at once
@@ -568,7 +569,7 @@ using namespace ws;
 extern "C" {
 
 size_t ws_logprobs_workspace_bytes(int rows, int V, int topk) {
-  if (rows < 1 || V < 1 || topk < 0 || topk > kMaxTop || topk > V) return 0;
+  if (rows < 1 || V < 1 || V > kMaxVocab || topk < 0 || topk > kMaxTop || topk > V) return 0;
   int splits, chunk;
   lp_split(rows, V, splits, chunk);
   if (splits == 1) return 256;
@@ -588,9 +589,9 @@ ws_status ws_token_logprobs(const void *logits, int dtype, long long ld, const i
     set_error("dtype must be WS_DTYPE_F32, WS_DTYPE_BF16 or WS_DTYPE_F16");
     return WS_ERR_ARG;
   }
-  if (rows < 1 || V < 1 || ld < V || topk < 0 || topk > kMaxTop || topk > V) {
-    set_error("log-probabilities: rows and V at least 1, ld at least V, topk 0..%d and at most V",
-              kMaxTop);
+  if (rows < 1 || V < 1 || V > kMaxVocab || ld < V || topk < 0 || topk > kMaxTop || topk > V) {
+    set_error("log-probabilities: rows and V at least 1 (V to 2^28), ld at least V, topk 0..%d and "
+              "at most V", kMaxTop);
     return WS_ERR_SHAPE;
   }
   if (((uintptr_t)logits & (dtype == WS_DTYPE_F32 ? 3u : 1u)) || ((uintptr_t)workspace & 15u)) {

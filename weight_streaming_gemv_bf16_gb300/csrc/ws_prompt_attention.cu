@@ -355,23 +355,24 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       // rows to the tile's query buffer (its products are done), 16-byte
       // pieces in an order that spreads over the banks, then out row by row
       unsigned char* st = sq + tile * kPaTileBytes + (warp & 3) * 32 * 256;
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o[32];
-        tmem_ld32(to + 32 * c, o);
-        tmem_wait_ld();
-        tmem_loaded<32>(o);
-        if (odd && tok < len) pa_odd_values<DT>(a, &sh, first, tok, guard0, head, kvh, m, 32 * c, o);
+      uint32_t o[128];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t w[4];
+      for (int c = 0; c < 4; ++c) tmem_ld32(to + 32 * c, o + 32 * c);
+      tmem_wait_ld();
+      tmem_loaded<128>(o);
+      if (odd && tok < len) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = pa_pack<DT>(__uint_as_float(o[8 * i + 2 * e]) * inv,
-                               __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-          const int piece = (4 * c + i) ^ (lane & 7);
-          *reinterpret_cast<uint4*>(st + lane * 256 + piece * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        for (int c = 0; c < 4; ++c)
+          pa_odd_values<DT>(a, &sh, first, tok, guard0, head, kvh, m, 32 * c, o + 32 * c);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = pa_pack<DT>(__uint_as_float(o[8 * i + 2 * e]) * inv,
+                             __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+        *reinterpret_cast<uint4*>(st + lane * 256 + (i ^ (lane & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
       }
       if (a.lse && tok < len)
         a.lse[(size_t)(first + tok) * a.nh + head] = (m + log2f(sum)) * 0.6931471805599453f;
