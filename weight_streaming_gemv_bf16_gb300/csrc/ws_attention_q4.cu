@@ -145,8 +145,9 @@ __device__ __noinline__ void q4_stage_last(const AttnQ4Params& a, size_t seg, in
   load8<DT_F32>((keys ? a.k_new : a.v_new) + seg * kKvDim + (lane & 15) * 8, x);
   uint32_t sz;
   const uint32_t w = quantize8(x, sz);
-  put_row(st + ((keys ? 0 : kQ4Tile) + n) * kKvRow, w, sz, keys, true);
-  put_row((keys ? kr : vr) + n * kKvRow, w, sz, keys, true);
+  const KvLane at(keys);
+  put_row(st + ((keys ? 0 : kQ4Tile) + n) * kKvRow, w, sz, at);
+  put_row((keys ? kr : vr) + n * kKvRow, w, sz, at);
   uint4* z = reinterpret_cast<uint4*>(st + (keys ? 0 : kQ4Tile * kKvRow));
   for (int i = (n + 1) * 5 + (lane & 15); i < kQ4Tile * 5; i += 16) z[i] = make_uint4(0, 0, 0, 0);
   __syncwarp();

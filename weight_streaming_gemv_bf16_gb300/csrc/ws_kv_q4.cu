@@ -79,8 +79,10 @@ __global__ void __launch_bounds__(kKvWarps * 32, 4) k_kv_store_q4(const __grid_c
   const char* src = static_cast<const char*>(keys ? a.k : a.v) + ((size_t)g * kKvDim + (lane & 15) * 8) * es;
   const size_t stride = (size_t)(keys ? a.ks : a.vs) * es;
   unsigned char* cache = keys ? a.kc : a.vc;
+  const KvLane at(keys);
+  src += (size_t)base * stride;
   KvPlace place = {0, 0, 0, false, 0};
-  for (int i = 0; i < a.per; i += kKvBatch) {
+  for (int i = 0; i < a.per; i += kKvBatch, src += kKvBatch * kKvWarps * stride) {
     uint4 raw[kKvBatch][DT == DT_F32 ? 2 : 1];
     unsigned char* dst[kKvBatch];
 #pragma unroll
@@ -90,7 +92,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, 4) k_kv_store_q4(const __grid_c
       if (i + u < a.per && t < a.T) {
 #pragma unroll
         for (int e = 0; e < (DT == DT_F32 ? 2 : 1); ++e)
-          raw[u][e] = __ldcs(reinterpret_cast<const uint4*>(src + t * stride) + e);
+          raw[u][e] = __ldcs(reinterpret_cast<const uint4*>(src + u * kKvWarps * stride) + e);
         if (t < place.lo || t >= place.hi) kv_find(a, t, g, place);
         if (t < place.lim) dst[u] = cache + (place.at + (t - place.lo)) * kKvRow;
         else if (place.over && lane == 0) atomicExch(a.err, kDerrBadSlot);
@@ -103,7 +105,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, 4) k_kv_store_q4(const __grid_c
       load8<DT>(raw[u], x);
       uint32_t sz;
       const uint32_t w = quantize8(x, sz);
-      put_row(dst[u], w, sz, keys, true);
+      put_row(dst[u], w, sz, at);
     }
   }
 }
@@ -117,9 +119,12 @@ __global__ void __launch_bounds__(kKvWarps * 32) k_kv_load_q4(const __grid_const
   const bool keys = lane < 16;
   constexpr size_t es = DT == DT_F32 ? 4 : 2;
   const unsigned char* cache = keys ? a.kc : a.vc;
-  char* out = static_cast<char*>(keys ? a.k_out : a.v_out) + ((size_t)g * kKvDim + (lane & 15) * 8) * es;
+  const size_t stride = (size_t)a.nkv * kKvDim * es;
+  char* out = static_cast<char*>(keys ? a.k_out : a.v_out) + (size_t)base * stride +
+              ((size_t)g * kKvDim + (lane & 15) * 8) * es;
+  const KvLane at(keys);
   KvPlace place = {0, 0, 0, false, 0};
-  for (int i = 0; i < a.per; i += kKvBatch) {
+  for (int i = 0; i < a.per; i += kKvBatch, out += kKvBatch * kKvWarps * stride) {
     KvWord word[kKvBatch];
     bool there[kKvBatch];
 #pragma unroll
@@ -129,7 +134,7 @@ __global__ void __launch_bounds__(kKvWarps * 32) k_kv_load_q4(const __grid_const
       if (!there[u]) continue;
       if (t < place.lo || t >= place.hi) kv_find(a, t, g, place);
       there[u] = t < place.lim;
-      if (there[u]) word[u] = get_word(cache + (place.at + (t - place.lo)) * kKvRow, keys);
+      if (there[u]) word[u] = get_word(cache + (place.at + (t - place.lo)) * kKvRow, at);
       else if (place.over && lane == 0) atomicExch(a.err, kDerrBadSlot);
     }
 #pragma unroll
@@ -137,7 +142,7 @@ __global__ void __launch_bounds__(kKvWarps * 32) k_kv_load_q4(const __grid_const
       if (!there[u]) continue;
       float x[8];
       word_values(word[u], x);
-      store8<DT>(out + (size_t)(base + (i + u) * kKvWarps) * a.nkv * kKvDim * es, x);
+      store8<DT>(out + u * kKvWarps * stride, x);
     }
   }
 }

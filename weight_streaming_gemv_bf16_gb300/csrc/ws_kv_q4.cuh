@@ -165,28 +165,33 @@ __device__ __forceinline__ uint32_t quantize8(float (&x)[8], uint32_t& sz) {
   return w;
 }
 
-// The row's 80 bytes from 16 lanes' quantize8 results: lane l = 4 g + t of the
-// half warp holds the codes of group g.  `row` in global or shared memory,
-// 4-byte aligned; write = false takes part in the exchange only.
-__device__ __forceinline__ void put_row(unsigned char* row, uint32_t w, uint32_t sz, bool keys,
-                                        bool write) {
-  const int l = threadIdx.x & 15, g = l >> 2, t = l & 3;
-  // values: the pair of groups (g, g ^ 1) trades halves, so that each lane
-  // writes the two units of one r
-  const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 4);
-  int at = 4 * t + g;
-  if (!keys) {
-    if (g & 1) {
-      w = (other >> 16) | (w & 0xffff0000u);
-      at = (2 * t + 1) * 2 + (g >> 1);
-    } else {
-      w = (w & 0xffffu) | (other << 16);
-      at = (2 * t) * 2 + (g >> 1);
-    }
+// Where lane l = 4 g + t of a row's 16 lanes finds and leaves its codes: the
+// same instructions for keys and values, which lanes of one warp may hold both.
+// Keys: 32-bit word 4 t + g.  Values: units 8 t + g and 8 t + 4 + g to read; to
+// write, the pair of groups (g, g ^ 1) trades halves, so that each lane has the
+// two units of one r, a word.
+struct KvLane {
+  int read0, read1;  // bytes of the two 16-bit units
+  int write;         // word
+  uint32_t pick;     // byte selector of (own, partner's) codes
+  int sz;            // word of the group's (s, z)
+  __device__ __forceinline__ KvLane(bool keys) {
+    const int l = threadIdx.x & 15, g = l >> 2, t = l & 3;
+    read0 = keys ? 4 * (4 * t + g) : 2 * (8 * t + g);
+    read1 = keys ? read0 + 2 : read0 + 8;
+    write = keys ? 4 * t + g : (2 * t + (g & 1)) * 2 + (g >> 1);
+    pick = keys ? 0x3210 : g & 1 ? 0x3276 : 0x5410;
+    sz = kKvCodes / 4 + g;
   }
-  if (!write) return;
-  reinterpret_cast<uint32_t*>(row)[at] = w;
-  if (t == 0) reinterpret_cast<uint32_t*>(row + kKvCodes)[g] = sz;
+};
+
+// The row's 80 bytes from 16 lanes' quantize8 results.  `row` in global or
+// shared memory, 4-byte aligned.
+__device__ __forceinline__ void put_row(unsigned char* row, uint32_t w, uint32_t sz, const KvLane& at) {
+  const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 4);
+  uint32_t* r = reinterpret_cast<uint32_t*>(row);
+  r[at.write] = __byte_perm(w, other, at.pick);
+  if ((threadIdx.x & 3) == 0) r[at.sz] = sz;
 }
 
 // What lane l of a row's 16 lanes reads: its eight codes and their (s, z); and
@@ -194,27 +199,25 @@ __device__ __forceinline__ void put_row(unsigned char* row, uint32_t w, uint32_t
 struct KvWord {
   uint32_t w, sz;
 };
-__device__ __forceinline__ KvWord get_word(const unsigned char* row, bool keys) {
-  const int l = threadIdx.x & 15, g = l >> 2, t = l & 3;
+__device__ __forceinline__ KvWord get_word(const unsigned char* row, const KvLane& at) {
   KvWord r;
-  if (keys) {
-    r.w = reinterpret_cast<const uint32_t*>(row)[4 * t + g];
-  } else {
-    const uint16_t* u = reinterpret_cast<const uint16_t*>(row);
-    r.w = u[4 * (2 * t) + g] | ((uint32_t)u[4 * (2 * t + 1) + g] << 16);
-  }
-  r.sz = reinterpret_cast<const uint32_t*>(row + kKvCodes)[g];
+  r.w = *reinterpret_cast<const uint16_t*>(row + at.read0) |
+        ((uint32_t)*reinterpret_cast<const uint16_t*>(row + at.read1) << 16);
+  r.sz = reinterpret_cast<const uint32_t*>(row)[at.sz];
   return r;
 }
 __device__ __forceinline__ void word_values(const KvWord& r, float (&x)[8]) {
   const float s = bf16lo(r.sz), z = bf16hi(r.sz);
   const uint32_t even = r.w & 0x0f0f0f0fu, odd = (r.w >> 4) & 0x0f0f0f0fu;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     // 2^23 + code, a byte into the mantissa; s (code - 8) is exact, so the fma
     // rounds where the sum does
-    const float c = __uint_as_float(__byte_perm(i & 1 ? odd : even, 0x4b000000u, 0x7540 | (i >> 1)));
-    x[i] = __fmaf_rn(s, __fsub_rn(c, 8388616.f), z);
+    const float2 c = make_float2(__uint_as_float(__byte_perm(even, 0x4b000000u, 0x7540 | i)),
+                                 __uint_as_float(__byte_perm(odd, 0x4b000000u, 0x7540 | i)));
+    const float2 v = fma2(make_float2(s, s), add2(c, make_float2(-8388616.f, -8388616.f)), make_float2(z, z));
+    x[2 * i] = v.x;
+    x[2 * i + 1] = v.y;
   }
 }
 
