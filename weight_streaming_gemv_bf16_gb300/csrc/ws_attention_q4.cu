@@ -2,7 +2,33 @@
 // token per batch row: the call of ws_attention.cu on rows of 80 bytes.
 //
 // out_h = sum_j p_j v_j, p = softmax_j(q_h . k_j / sqrt(128)) over the slots
-// 0 .. pos, k and v = s (code - 8) + z per slot and group of 32 dimensions.
+// 0 .. pos, k and v = s (code - 8) + z per slot and group of 32 dimensions, so
+//   q . k = sum_g s_g (sum_d q_d (code_d - 8)) + z_g (sum_d q_d),
+//   out   = sum_j (p_j s_j) (code_j - 8) + sum_j p_j z_j :
+// the codes enter the products as exact small integers, a key's scale weighs
+// each group's part of its score, and a value's scale joins the probability.
+// The fp32 operands (q, and p s) enter as bf16 hi + lo pairs, their errors
+// 2^-17.  Warp-level products (m16n8k16): a tile is 16 or 32 slots by 128
+// dimensions for at most 8 heads, far below a tcgen05 tile, and its operands
+// are made in registers.
+//
+// The tiles of 32 slots of all rows and heads are cut into one equal run a
+// resident CTA, whatever the rows' lengths; the CTA that shares a (row, head)
+// with others leaves a partial result, and the last of each 16 and the last of
+// those groups merge.  A warp streams its tiles through a ring of two stages
+// (two bulk copies of 2560 bytes each).
+//
+// Bound by instruction issue, not by DRAM: expanding 4 bits to operands and
+// carrying the scales takes about 800 instructions a warp and tile.  16 rows x
+// 16384 slots x 8 heads (32 query heads; 257 MB): 62.5 us, 4.1 TB/s, 0.61 of the
+// measured copy rate.  What it took from 113 us: nibbles masked in place and
+// raised by one packed fma (no shift for every second one) 93 -> 80; products
+// that start from nothing and two CTAs a SM without spills -> 73; for up to 4
+// heads the operands changed over -> 67; lo terms by the mixed fma -> 62.5.
+// Slower, not kept: keys as e4m3 (the masked nibbles are e4m3 numbers already,
+// the sums came out exact; mixing the two product types cost more than the
+// conversions) 90; nibbles as raw subnormal bf16 operands 72; four stages or
+// three, 8 warps a CTA, 4 CTAs a SM.
 #include <cmath>
 #include <mutex>
 
@@ -20,7 +46,8 @@ constexpr int kQ4Threads = kQ4Warps * 32;
 constexpr int kQ4Stages = 2;     // ring stages per warp
 constexpr int kQ4StageBytes = 2 * kQ4Tile * kKvRow;  // keys, then values
 constexpr int kQ4MaxCtas = 1024;
-constexpr int kQ4MinTiles = 1 * kQ4Warps;            // tiles a CTA takes at least
+constexpr int kQ4MinTiles = 1 * kQ4Warps;            // tiles a CTA takes at least (one sequence of 1000
+                                                     // slots: 10.5 us with 1 a warp, 11.9 with 2, 15.5 with 4)
 constexpr int kQ4Merge = 16;                         // partial results merged in one go
 constexpr int kQ4Part = kKvDim + 4;                  // one partial result: acc[128], max, sum, two unused
 constexpr int kQ4Ring = kQ4Warps * kQ4Stages * kQ4StageBytes;
@@ -419,11 +446,11 @@ __device__ __forceinline__ uint32_t q4_transpose(uint32_t a) {  // an 8x8 matrix
 // The same for up to 4 heads a group, with the operands changed over: the codes
 // are the rows (16 slots, then 16 dimensions), the columns the heads' hi terms
 // and, from 4 on, their lo terms.  Half as many products and accumulators, so
-// that twice the CTAs fit; the probabilities pass from rows to columns by a
+// that more CTAs fit; the probabilities pass from rows to columns by a
 // transposition between the two products.
 struct Q4Narrow {
   static constexpr int kHeads = 4;
-  static constexpr int kCtas = 3;
+  static constexpr int kCtas = 3;  // a SM: 62.8 us, two or four 64 and 67 (the latter spilled)
   struct Shared {};
   // lane: heads 2 (rt & 1) + e; o[2 g + i / 2]: dimensions 32 g + 4 rg + i, hi
   // terms for rt < 2, lo terms for the others
@@ -722,14 +749,16 @@ __global__ void __launch_bounds__(kQ4Threads, Core::kCtas)
       if (!__all_sync(0xffffffffu, ok)) {
         ok = ok || mbar_wait_bounded(&full[warp][nc], par, a.timeout_ns);
         if (__any_sync(0xffffffffu, !ok)) {
-          abort = true;
+          abort = true;  // nothing more is issued; what is under way ends first
           if (lane == 0) atomicExch(a.err, (int)DERR_TIMEOUT);
+          for (int i = 0; x + i * kQ4Warps < min(xi, run); ++i)
+            mbar_wait_bounded(&full[warp][nc ^ i], par ^ (nc & i), a.timeout_ns);
         }
       }
       if (!abort) core.tile(st, (x - cur.at) * kQ4Tile, cur.pos, shared);
       nc ^= 1;
       par ^= nc == 0;
-      issue();
+      if (!abort) issue();
     }
 
     // the four warps' results, then this CTA's

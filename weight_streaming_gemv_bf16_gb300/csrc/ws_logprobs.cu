@@ -2,7 +2,15 @@
 // with the row's entropy and its most likely tokens.
 //
 // With m = max x, Z = sum e^(x - m): log p_i = x_i - m - log Z, and the
-// entropy -sum p log p = log Z - sum e^(x - m) (x - m) / Z.
+// entropy -sum p log p = log Z - sum e^(x - m) (x - m) / Z.  One pass, a running
+// maximum per thread (2^x by the special-function unit, which takes x log2 e).
+//
+// Bound by instruction issue, then DRAM: 2048 rows x 151665 bf16 with 20
+// alternatives: 152 us, 4.07 TB/s, 0.60 of the measured copy rate; the sums
+// alone are 6 instructions a value, the search about as much again.  A small
+// batch's rows are cut into steps over up to 48 CTAs, the last of which merges:
+// 16 x 151936 fp32 11.9 us, 1 x 50257 10.7 us, all of it latency (a CTA a row:
+// 196 and 207 us).
 #include <cmath>
 #include <cstddef>
 #include <mutex>
