@@ -134,7 +134,7 @@ def test_binding_refuses_tensors_off_the_current_device_or_misshapen(lib, monkey
     kc = torch.zeros(2, 2, 10, 80, dtype=torch.uint8)
     st = torch.zeros(2, dtype=torch.int32)
     f, n = torch.zeros(2, 512), torch.zeros(2, 256)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(wb, "_here", lambda: 0)
     with pytest.raises(ValueError, match="current device"):
         wb.prompt_attention(q, kv, kv, cu, out)
     with pytest.raises(ValueError, match="current device"):
@@ -145,7 +145,7 @@ def test_binding_refuses_tensors_off_the_current_device_or_misshapen(lib, monkey
         wb.decode_attention_q4(f, n, n, kc, kc, st, kc, out_f32=f)
     with pytest.raises(ValueError, match="current device"):
         wb.token_logprobs(f, kc, entropy=torch.zeros(2))
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
+    monkeypatch.setattr(wb, "_here", lambda: -1)
     with pytest.raises(ValueError, match="heads must be contiguous"):
         wb.prompt_attention(q.transpose(0, 1), kv, kv, cu, out)
     with pytest.raises(ValueError, match="expected .tokens, heads"):

@@ -355,16 +355,28 @@ def decode_attention(q, k_new, v_new, k_cache, v_cache, pos, workspace, out_f32=
 # they are on the current device, where the library launches.  Each check hands
 # on the pointer (a step's calls are short enough for the host to matter).
 
+_I32, _F32, _U8, _BF16 = torch.int32, torch.float32, torch.uint8, torch.bfloat16
+_CODES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+_here = torch.cuda.current_device
+
+
 def _need(ok, what: str):
     if not ok:
         raise ValueError(what)
+
+
+def _code(dtype) -> int:
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
 
 
 def _at(t, dtype, shape, dev: int, what: str):
     """The address of a contiguous tensor of this type and shape; None passes."""
     if t is None:
         return None
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+    if t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
     if t.dtype is dtype and t.shape == shape and t.is_contiguous():
         raise ValueError(f"{what} on {t.device}: expected the current device, cuda:{dev}")
@@ -402,7 +414,7 @@ def prompt_attention(q, k, v, cu_seqlens, out, lse=None, stream=None):
     [T, n_kv, 128] in bf16 or fp16 (token strides free, so columns of one
     fused projection will do), cu_seqlens int32 [n_seqs + 1] on the device,
     out [T, n_heads * 128] of the same type, lse fp32 [T, n_heads] or None."""
-    dev = torch.cuda.current_device()
+    dev = _here()
     (T, nh, d), qs, qp = _tokens_at(q, dev, "q")
     kshape, ks, kp = _tokens_at(k, dev, "k")
     vshape, vs, vp = _tokens_at(v, dev, "v")
@@ -412,8 +424,8 @@ def prompt_attention(q, k, v, cu_seqlens, out, lse=None, stream=None):
     _need(k.dtype is dt and v.dtype is dt, "q, k and v disagree in type")
     n = cu_seqlens.shape[0]
     _check(load().ws_prompt_attention(
-        qp, kp, vp, _dtype_code(q), _at(cu_seqlens, torch.int32, (n,), dev, "cu_seqlens"),
-        _at(out, dt, (T, nh * d), dev, "out"), _at(lse, torch.float32, (T, nh), dev, "lse"), T,
+        qp, kp, vp, _code(dt), _at(cu_seqlens, _I32, (n,), dev, "cu_seqlens"),
+        _at(out, dt, (T, nh * d), dev, "out"), _at(lse, _F32, (T, nh), dev, "lse"), T,
         n - 1, nh, nkv, d, qs, ks, vs, _stream_on(stream, dev)))
 
 
@@ -426,7 +438,7 @@ def kv_q4_row_bytes(head_dim=128) -> int:
 
 def new_kv_cache_q4(n_rows, n_kv_heads, s_max, head_dim=128, device="cuda"):
     """One 4-bit cache (keys or values): uint8 [n_rows, n_kv, s_max, 80]."""
-    return torch.zeros((n_rows, n_kv_heads, s_max, kv_q4_row_bytes(head_dim)), dtype=torch.uint8,
+    return torch.zeros((n_rows, n_kv_heads, s_max, kv_q4_row_bytes(head_dim)), dtype=_U8,
                        device=device)
 
 
@@ -435,11 +447,11 @@ def _kv_q4_args(nkv, k_cache, v_cache, start, cu_seqlens, rows, dev):
     _need(len(shape) == 4 and shape[3] == _KV_Q4_ROW and shape[1] == nkv,
           "k_cache: expected [rows, n_kv, s_max, 80]")
     n = start.shape[0]
-    return (_at(cu_seqlens, torch.int32, (n + 1,), dev, "cu_seqlens"),
-            _at(rows, torch.int32, (n,), dev, "rows"),
-            _at(start, torch.int32, (n,), dev, "start"),
-            _at(k_cache, torch.uint8, shape, dev, "k_cache"),
-            _at(v_cache, torch.uint8, shape, dev, "v_cache"), n, shape[0], shape[2])
+    return (_at(cu_seqlens, _I32, (n + 1,), dev, "cu_seqlens"),
+            _at(rows, _I32, (n,), dev, "rows"),
+            _at(start, _I32, (n,), dev, "start"),
+            _at(k_cache, _U8, shape, dev, "k_cache"),
+            _at(v_cache, _U8, shape, dev, "v_cache"), n, shape[0], shape[2])
 
 
 def kv_store_q4(k, v, k_cache, v_cache, start, cu_seqlens=None, rows=None, stream=None):
@@ -447,21 +459,22 @@ def kv_store_q4(k, v, k_cache, v_cache, start, cu_seqlens=None, rows=None, strea
     [n_rows, n_kv, s_max, 80] from slot start[i] on of cache row rows[i] (i
     without `rows`) for the tokens cu_seqlens[i] .. cu_seqlens[i + 1] - 1
     (token i alone without `cu_seqlens`)."""
-    dev = torch.cuda.current_device()
+    dev = _here()
     shape, ks, kp = _tokens_at(k, dev, "k")
     vshape, vs, vp = _tokens_at(v, dev, "v")
-    _need(vshape == shape and v.dtype is k.dtype, "k and v disagree")
+    dt = k.dtype
+    _need(vshape == shape and v.dtype is dt, "k and v disagree")
     T, nkv, d = shape
     cu, rw, st, kc, vc, n, n_rows, s_max = _kv_q4_args(nkv, k_cache, v_cache, start, cu_seqlens,
                                                        rows, dev)
-    _check(load().ws_kv_store_q4(kp, vp, _dtype_code(k), cu, rw, st, kc, vc, T, n, n_rows, nkv, d,
+    _check(load().ws_kv_store_q4(kp, vp, _code(dt), cu, rw, st, kc, vc, T, n, n_rows, nkv, d,
                                  s_max, ks, vs, _stream_on(stream, dev)))
 
 
 def kv_load_q4(k_cache, v_cache, start, k, v, cu_seqlens=None, rows=None, stream=None):
     """The values that cached rows stand for, to k and v [T, n_kv, 128] (fp32,
     bf16 or fp16, contiguous); the other arguments as for kv_store_q4."""
-    dev = torch.cuda.current_device()
+    dev = _here()
     shape, dt = k.shape, k.dtype
     _need(len(shape) == 3, "k: expected [tokens, heads, head_dim]")
     T, nkv, d = shape
@@ -469,7 +482,7 @@ def kv_load_q4(k_cache, v_cache, start, k, v, cu_seqlens=None, rows=None, stream
     vp = _at(v, dt, shape, dev, "v")
     cu, rw, st, kc, vc, n, n_rows, s_max = _kv_q4_args(nkv, k_cache, v_cache, start, cu_seqlens,
                                                        rows, dev)
-    _check(load().ws_kv_load_q4(kc, vc, cu, rw, st, kp, vp, _dtype_code(k), T, n, n_rows, nkv, d,
+    _check(load().ws_kv_load_q4(kc, vc, cu, rw, st, kp, vp, _code(dt), T, n, n_rows, nkv, d,
                                 s_max, _stream_on(stream, dev)))
 
 
@@ -482,21 +495,21 @@ def decode_attention_q4(q, k_new, v_new, k_cache, v_cache, pos, workspace, out_f
     """decode_attention over the 4-bit caches uint8 [B, n_kv, s_max, 80]: q
     [B, n_heads*128] fp32, k_new/v_new [B, n_kv*128] fp32 (quantised into the
     caches at pos), pos int32 [B] on the device (negative: no sequence)."""
-    dev = torch.cuda.current_device()
+    dev = _here()
     shape = k_cache.shape
     _need(len(shape) == 4 and shape[3] == _KV_Q4_ROW, "k_cache: expected [B, n_kv, s_max, 80]")
     B, nkv, s_max, _ = shape
-    d, f32 = 128, torch.float32
+    d = 128
     nh = q.shape[-1] // d
     new = (B, nkv * d)
     heads = (B, nh * d)
     wp, wb = _space_at(workspace, dev)
     _check(load().ws_decode_attention_q4(
-        _at(q, f32, heads, dev, "q"), _at(k_new, f32, new, dev, "k_new"),
-        _at(v_new, f32, new, dev, "v_new"), _at(k_cache, torch.uint8, shape, dev, "k_cache"),
-        _at(v_cache, torch.uint8, shape, dev, "v_cache"),
-        _at(pos, torch.int32, (B,), dev, "pos"), _at(out_f32, f32, heads, dev, "out_f32"),
-        _at(out_bf16, torch.bfloat16, heads, dev, "out_bf16"), B, nh, nkv, d, s_max, wp, wb,
+        _at(q, _F32, heads, dev, "q"), _at(k_new, _F32, new, dev, "k_new"),
+        _at(v_new, _F32, new, dev, "v_new"), _at(k_cache, _U8, shape, dev, "k_cache"),
+        _at(v_cache, _U8, shape, dev, "v_cache"),
+        _at(pos, _I32, (B,), dev, "pos"), _at(out_f32, _F32, heads, dev, "out_f32"),
+        _at(out_bf16, _BF16, heads, dev, "out_bf16"), B, nh, nkv, d, s_max, wp, wb,
         _stream_on(stream, dev)))
 
 
@@ -509,20 +522,20 @@ def token_logprobs(logits, workspace, targets=None, logprob=None, entropy=None, 
     """Log-probabilities over logits [rows, V] (fp32, bf16 or fp16; rows may be
     padded): logprob fp32 [rows] of targets int32 [rows], entropy fp32 [rows],
     top_idx int32 and top_logprob fp32 [rows, topk]; each output may be None."""
-    dev = torch.cuda.current_device()
+    dev = _here()
     rows, V = logits.shape
     st, s1 = logits.stride()
     _need(s1 == 1 or V == 1, "logits: a row's values must be contiguous")
     _need(logits.get_device() == dev, f"logits on {logits.device}: expected the current device")
     top = top_idx if top_idx is not None else top_logprob
     topk = 0 if top is None else top.shape[-1]
-    f32, i32, row, alt = torch.float32, torch.int32, (rows,), (rows, topk)
+    row, alt = (rows,), (rows, topk)
     wp, wb = _space_at(workspace, dev)
     _check(load().ws_token_logprobs(
-        logits.data_ptr(), _dtype_code(logits), st if rows > 1 else V,
-        _at(targets, i32, row, dev, "targets"), _at(logprob, f32, row, dev, "logprob"),
-        _at(entropy, f32, row, dev, "entropy"), _at(top_idx, i32, alt, dev, "top_idx"),
-        _at(top_logprob, f32, alt, dev, "top_logprob"), rows, V, topk, wp, wb,
+        logits.data_ptr(), _code(logits.dtype), st if rows > 1 else V,
+        _at(targets, _I32, row, dev, "targets"), _at(logprob, _F32, row, dev, "logprob"),
+        _at(entropy, _F32, row, dev, "entropy"), _at(top_idx, _I32, alt, dev, "top_idx"),
+        _at(top_logprob, _F32, alt, dev, "top_logprob"), rows, V, topk, wp, wb,
         _stream_on(stream, dev)))
 
 
