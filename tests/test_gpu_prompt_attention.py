@@ -192,6 +192,26 @@ def test_bounds_out_of_range_are_skipped_and_flagged():
             _check(q, k, v, ok, out, lse)
 
 
+@pytest.mark.parametrize("at", [0, 31, 32, 50, 69])
+def test_one_bad_bound_among_many_sequences(at):
+    """70 sequences of 3 tokens, one of them with an end past the tokens (and so
+    a start past them for the next): both are skipped and flagged."""
+    q, k, v = _inputs(210, 2, 1, torch.bfloat16, at)
+    bounds = list(range(0, 211, 3))
+    bounds[at + 1] = 100000
+    out, lse = _call(q, k, v, bounds)
+    assert wb.device_error(reset=True) == 3
+    good = [(3 * i, 3 * i + 3) for i in range(70) if i not in (at, at + 1)]
+    ref, mag, _ = sv.prompt_attention(*(x.double().numpy() for x in (q, k, v)),
+                                      list(range(0, 211, 3)))
+    got = out.double().numpy().reshape(210, 2, D)
+    rows = np.zeros(210, bool)
+    for a, b in good:
+        rows[a:b] = True
+    assert (got[~rows] == 7.0).all()
+    assert (np.abs(got - ref)[rows] <= (U[torch.bfloat16] * (mag + np.abs(ref)) * 1.01 + 1e-6)[rows]).all()
+
+
 def test_long_sequence_against_the_gpu_in_64_bits():
     """2100 tokens: many tiles of keys per row."""
     q, k, v = _inputs(2100, 4, 2, torch.bfloat16, 99)

@@ -127,7 +127,9 @@ __device__ __forceinline__ bool pa_place(const PromptParams& a, int t, int rows,
       lo = a.cu[i];
       hi = a.cu[i + 1];
       if (lo < 0 || hi < lo || hi > a.T) {
-        if (blockIdx.x == 0 && threadIdx.x < 32) atomicExch(a.err, kDerrBadSeq);
+        // (every CTA that gets this far: there is one more of them than tiles for
+        // each sequence without tiles)
+        if (threadIdx.x < 32) atomicExch(a.err, kDerrBadSeq);
         lo = hi = 0;
       }
     }
