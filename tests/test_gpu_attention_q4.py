@@ -107,6 +107,24 @@ def test_ragged_batches(B):
     _run(B, 12, 2, 640, pos, B)
 
 
+# 96 rows and 8 heads: more (row, head)s than CTAs are resident on the device,
+# so one CTA works through several short ones, some of its warps on none of them
+@pytest.mark.parametrize("nh", [8, 40])
+@pytest.mark.parametrize("top", [1, 33, 65, 130])
+def test_many_short_sequences(nh, top):
+    r = np.random.default_rng(nh + top)
+    pos = r.integers(-1, top, 96).tolist()
+    pos[:3] = [top - 1, 0, -1]
+    _run(96, nh, 8, top, pos, nh + top)
+
+
+def test_many_short_sequences_and_a_long_one():
+    r = np.random.default_rng(11)
+    pos = r.integers(0, 160, 70).tolist()
+    pos[35] = 4999
+    _run(70, 12, 4, 5000, pos, 11)
+
+
 def test_long_cache_in_many_splits():
     _run(1, 12, 2, 40000, [39999], 3)
     _run(2, 8, 8, 9001, [9000, 17], 4)

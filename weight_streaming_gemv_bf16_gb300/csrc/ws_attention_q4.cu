@@ -12,19 +12,20 @@
 // dimensions for at most 8 heads, far below a tcgen05 tile, and its operands
 // are made in registers.
 //
-// The tiles of 32 slots of all rows and heads are cut into one equal run a
-// resident CTA, whatever the rows' lengths; the CTA that shares a (row, head)
+// The tiles of 32 slots of all rows and heads, in fours, are cut into one equal
+// run a resident CTA, whatever the rows' lengths; the CTA that shares a (row, head)
 // with others leaves a partial result, and the last of each 16 and the last of
 // those groups merge.  A warp streams its tiles through a ring of two stages
 // (two bulk copies of 2560 bytes each).
 //
 // Bound by instruction issue, not by DRAM: expanding 4 bits to operands and
 // carrying the scales takes about 800 instructions a warp and tile.  16 rows x
-// 16384 slots x 8 heads (32 query heads; 257 MB): 62.5 us, 4.1 TB/s, 0.61 of the
+// 16384 slots x 8 heads (32 query heads; 257 MB): 61.7 us, 4.2 TB/s, 0.62 of the
 // measured copy rate.  What it took from 113 us: nibbles masked in place and
 // raised by one packed fma (no shift for every second one) 93 -> 80; products
 // that start from nothing and two CTAs a SM without spills -> 73; for up to 4
-// heads the operands changed over -> 67; lo terms by the mixed fma -> 62.5.
+// heads the operands changed over -> 67; lo terms by the mixed fma -> 63.4; runs
+// cut between fours of tiles -> 61.7.
 // Slower, not kept: keys as e4m3 (the masked nibbles are e4m3 numbers already,
 // the sums came out exact; mixing the two product types cost more than the
 // conversions) 90; nibbles as raw subnormal bf16 operands 72; four stages or
@@ -46,8 +47,6 @@ constexpr int kQ4Threads = kQ4Warps * 32;
 constexpr int kQ4Stages = 2;     // ring stages per warp
 constexpr int kQ4StageBytes = 2 * kQ4Tile * kKvRow;  // keys, then values
 constexpr int kQ4MaxCtas = 1024;
-constexpr int kQ4MinTiles = 1 * kQ4Warps;            // tiles a CTA takes at least (one sequence of 1000
-                                                     // slots: 10.5 us with 1 a warp, 11.9 with 2, 15.5 with 4)
 constexpr int kQ4Merge = 16;                         // partial results merged in one go
 constexpr int kQ4Part = kKvDim + 4;                  // one partial result: acc[128], max, sum, two unused
 constexpr int kQ4Ring = kQ4Warps * kQ4Stages * kQ4StageBytes;
@@ -71,8 +70,15 @@ struct AttnQ4Params {
   unsigned long long timeout_ns;
 };
 
+// Tiles of a row and head in the count that the CTAs share out: a multiple of
+// the warps, which take four tiles in the time of one, so that a run never ends
+// among the four and short sequences get a CTA each.  Those past the last slot
+// are empty.  Counting the filled ones only, four to a CTA at least: 12 rows of 3
+// slots, 56/8 heads, 13.4 us against 7.2; 10 rows to 3190, 4/4, 15.4 against 14.2;
+// 16 x 16384, 32/8, 63.4 against 61.7; one row of 1000, 12/2, 8.80 against 8.85.
 __device__ __forceinline__ int q4_tiles(int pos, int S) {
-  return pos < 0 || pos >= S ? 0 : pos / kQ4Tile + 1;
+  constexpr int kSlots = kQ4Tile * kQ4Warps;
+  return pos < 0 || pos >= S ? 0 : (pos / kSlots + 1) * kQ4Warps;
 }
 
 // Two codes, nibble HI of byte 0 and of byte 2 of m, as bf16 f (code - 8) with
@@ -136,7 +142,7 @@ __device__ __forceinline__ unsigned q4_ticket(unsigned* p) {
 }
 
 // Where a warp's next tile lies: tile x of the CTA's range (counted from the
-// range's start) is tile x - at of (row b, head g), which has nt tiles.
+// range's start) is tile x - at of (row b, head g), which has nt of them.
 struct Q4Cursor {
   int b, g, at, nt, pos;
 };
@@ -651,7 +657,8 @@ __global__ void __launch_bounds__(kQ4Threads, Core::kCtas)
   pdl_wait();
   // the tiles of all rows and heads, cut into as many equal runs as there are
   // CTAs; every warp finds the run's place by itself
-  // (fewer than 2^31 of them: a tile is 5120 bytes of cache)
+  // (fewer than 2^31 of them: the caller's bound of 2^30, and three empty ones for
+  // each of 1024 * 65535 rows and heads at most)
   int total = 0, p0 = -1;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int p = b0 + lane < a.B ? a.pos[b0 + lane] : -1;
@@ -660,7 +667,7 @@ __global__ void __launch_bounds__(kQ4Threads, Core::kCtas)
     total += q4_tiles(p, a.S);
   }
   total = __reduce_add_sync(0xffffffffu, total) * a.nkv;
-  const int per = max((int)((total + gridDim.x - 1) / gridDim.x), kQ4MinTiles);
+  const int per = ((int)((total + gridDim.x - 1) / gridDim.x) + kQ4Warps - 1) / kQ4Warps * kQ4Warps;
   const int start = blockIdx.x * per, run = min(per, total - start);
   if (run <= 0) return;
   Q4Cursor cur;
@@ -704,11 +711,13 @@ __global__ void __launch_bounds__(kQ4Threads, Core::kCtas)
   unsigned char *ikr = nullptr, *ivr = nullptr;
   int ilast = -1;  // the last tile of the segment, counted as x
   auto issue = [&]() {
-    if (xi < run) {
+    for (; xi < run; xi += kQ4Warps) {
       if (xi > ilast) {
         q4_seek(a, ic, xi);
-        ilast = ic.at + ic.nt - 1;
-        const size_t row = ((size_t)ic.b * a.nkv + ic.g) * a.S + (size_t)(xi - ic.at) * kQ4Tile;
+        const int tile = xi - ic.at;
+        if (tile > ic.pos / kQ4Tile) continue;  // empty: on to the next row or head
+        ilast = ic.at + ic.pos / kQ4Tile;
+        const size_t row = ((size_t)ic.b * a.nkv + ic.g) * a.S + (size_t)tile * kQ4Tile;
         ikr = a.kc + row * kKvRow;
         ivr = a.vc + row * kKvRow;
       }
@@ -727,8 +736,9 @@ __global__ void __launch_bounds__(kQ4Threads, Core::kCtas)
       ni ^= 1;
       ikr += kQ4Warps * kQ4Tile * kKvRow;
       ivr += kQ4Warps * kQ4Tile * kKvRow;
+      xi += kQ4Warps;
+      return;
     }
-    xi += kQ4Warps;
   };
   static_assert(kQ4Stages == 2, "stage indices flip");
   issue();
@@ -742,7 +752,8 @@ __global__ void __launch_bounds__(kQ4Threads, Core::kCtas)
     const int x1 = min(run, cur.at + cur.nt);
     Core core;
     core.begin(a, cur.b, cur.g, shared);
-    for (; x < x1; x += kQ4Warps) {
+    const int xe = min(x1, cur.at + cur.pos / kQ4Tile + 1);
+    for (; x < xe; x += kQ4Warps) {
       const unsigned char* st = ring + nc * kQ4StageBytes;
       bool ok = abort || mbar_try_wait(&full[warp][nc], par);
       if (!__all_sync(0xffffffffu, ok)) {
@@ -750,7 +761,8 @@ __global__ void __launch_bounds__(kQ4Threads, Core::kCtas)
         if (__any_sync(0xffffffffu, !ok)) {
           abort = true;  // nothing more is issued; what is under way ends first
           if (lane == 0) atomicExch(a.err, (int)DERR_TIMEOUT);
-          for (int i = 0; x + i * kQ4Warps < min(xi, run); ++i)
+          // (both stages when the next to fill is the one waited for, else that one)
+          for (int i = 0; i < 2 - (ni ^ nc); ++i)
             mbar_wait_bounded(&full[warp][nc ^ i], par ^ (nc & i), a.timeout_ns);
         }
       }
@@ -759,6 +771,7 @@ __global__ void __launch_bounds__(kQ4Threads, Core::kCtas)
       par ^= nc == 0;
       if (!abort) issue();
     }
+    if (x < x1) x += kQ4Warps;  // an empty tile ends the row and head
 
     // (let go any earlier, the next kernel's CTAs take from this one's loads: 65.2
     // against 63.4 us over 16 x 16384 slots)
