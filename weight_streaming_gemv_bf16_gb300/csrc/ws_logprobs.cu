@@ -370,8 +370,9 @@ __global__ void __launch_bounds__(kLpThreads, 8) k_token_logprobs(const __grid_c
       float2 z = make_float2(0.f, 0.f), e2 = z;
 #pragma unroll
       for (int i = 0; i < kEach; i += 2) {
-        const float2 y = make_float2(max_nan(cur.diff(i, nm), kLpFar) * kLog2e,
-                                     max_nan(cur.diff(i + 1, nm), kLpFar) * kLog2e);
+        const float2 y = mul2(make_float2(max_nan(cur.diff(i, nm), kLpFar),
+                                          max_nan(cur.diff(i + 1, nm), kLpFar)),
+                              make_float2(kLog2e, kLog2e));
         const float2 e = make_float2(lp_exp2(y.x), lp_exp2(y.y));
         z = add2(z, e);
         e2 = fma2(e, y, e2);
