@@ -254,3 +254,16 @@ def test_more_candidates_than_there_is_room_for(dtype):
         got = _call(rows.cuda(), 32, t)
         _check(rows[:3], 32, t[:3], {n: v[:3] for n, v in got.items()})
         _check(rows[-3:], 32, t[-3:], {n: v[-3:] for n, v in got.items()})
+
+
+@pytest.mark.parametrize("k", [0, 5, 32])
+def test_row_counts_around_the_cuts_on_one_workspace(k):
+    """Rows of three steps over three, two and one CTA each, one call after the
+    other on the same workspace."""
+    V, counts = 9001, [405, 406, 608, 609, 1216, 1217]
+    ws = torch.zeros(max(wb.logprobs_workspace_bytes(n, V, k) for n in counts), dtype=torch.uint8,
+                     device="cuda")
+    for n in counts + counts[:1]:
+        x = _logits(n, V, torch.bfloat16, n)
+        t = _targets(n, V, n)
+        _check(x, k, t, _call(x.cuda(), k, t, ws=ws))

@@ -6,7 +6,7 @@
 // maximum per thread (2^x by the special-function unit, which takes x log2 e).
 //
 // Bound by instruction issue, then DRAM: 2048 rows x 151665 bf16 with 20
-// alternatives: 152 us, 4.07 TB/s, 0.60 of the measured copy rate; the sums
+// alternatives: 150 us, 4.14 TB/s, 0.61 of the measured copy rate; the sums
 // alone are 6 instructions a value, the search about as much again.  A small
 // batch's rows are cut into steps over up to 48 CTAs, the last of which merges:
 // 16 x 151936 fp32 11.9 us, 1 x 50257 10.7 us, all of it latency (a CTA a row:
@@ -31,7 +31,7 @@ constexpr int kLpStages = 2;        // steps on their way or worked on
 constexpr int kLpCompact = 64;      // candidates that make the CTA sort out the best ones
 constexpr int kLpBuf = 512;         // candidates there is room for
 constexpr int kLpSplits = 48;       // CTAs a row at most
-constexpr int kLpCtas = 608;        // CTAs that a small batch's rows are cut into
+constexpr int kLpCtas = 8 * 152;    // CTAs that a batch's rows are cut into: all that are resident
 constexpr float kLpFar = -1e4f;     // e^y is 0 long before: stands for -infinity in sums
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -529,7 +529,11 @@ __global__ void __launch_bounds__(kLpThreads, 8) k_token_logprobs(const __grid_c
 }
 
 // Splits of a row, and values a split: whole steps, and no more than fill
-// kLpCtas CTAs with all rows (a row alone on one CTA takes 40 times as long).
+// kLpCtas CTAs with all rows, one wave (a row alone on one CTA takes 20 times as
+// long).  With 608, 1216 and 1824 CTAs: 64 x 151936 bf16, 20 alternatives, 23.4,
+// 17.0, 17.0 us; 377 x 20034 fp32, 5 alternatives, 19.5, 15.9, 16.1; 558 x 75974
+// fp16 without, 26.1, 19.9, 23.6.  More rows are not cut, to even out their waves
+// either: 2048 x 151665, 20 alternatives, 151.5 us whole, 174.8 in halves.
 static void lp_split(int rows, int V, int& splits, int& chunk) {
   const int steps = (V + kLpStep - 1) / kLpStep;
   int want = kLpCtas / rows;
