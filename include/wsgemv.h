@@ -263,7 +263,9 @@ ws_status ws_prompt_attention(const void *q, const void *k, const void *v, int d
  * [n_seqs] on the device): negative skips the sequence.  Tokens outside every
  * sequence are skipped; one whose row is outside 0 .. n_rows - 1 or whose
  * slot is outside 0 .. s_max - 1 is skipped and raises the device error flag
- * (2).  Two tokens of one call must not share a slot.
+ * (2).  Bounds must not fall: where they do, a token may go with another
+ * sequence or be skipped, without a flag, but to no place outside the cache.
+ * Two tokens of one call must not share a slot.
  * ws_kv_load_q4: the reverse, with the same arguments: the values that the
  * rows stand for, rounded once to dtype, to k and v contiguous [T][n_kv_heads]
  * [128]; skipped tokens are left as they were.
@@ -697,6 +699,13 @@ long ws_debug_gemv_copies(int M, int K, int B, int nmat, int allow_split, int ct
  * would not take that kernel. */
 long ws_debug_gemv_copies_q4(int M, int K, int B, int nmat, int cta, int mma,
                              long long *triples, long max_triples, ws_gemv_schedule *sched);
+
+/* Where ws_kv_store_q4 and ws_kv_load_q4 find each token of one head, by the
+ * kernels' own code on host arrays: places[t] = row * s_max + slot, -1 for a
+ * token that is skipped, -2 for one that raises the error flag.  Returns how
+ * many have a place, -1 for bad arguments (host only). */
+long ws_debug_kv_places(const int32_t *cu_seqlens, const int32_t *rows, const int32_t *start, int T,
+                        int n_seqs, int n_rows, int s_max, long long *places);
 
 /* Read-only streaming kernel over [ptr, ptr + bytes): a read-roofline probe.
  * Writes one checksum per CTA into sink (uint32 [blocks]). */

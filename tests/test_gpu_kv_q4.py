@@ -210,3 +210,34 @@ def test_graph_replay_and_another_stream():
         assert np.array_equal(kc[:, :, step + 1].cpu().numpy(), sv.quantize_rows(k.numpy(), True))
         assert np.array_equal(
             vb.cpu().numpy(), sv.dequantize_rows(sv.quantize_rows(v.numpy(), False), False))
+
+
+@pytest.mark.parametrize("low", [-2147483643, -2147483648])
+def test_bounds_far_below_the_tokens(low):
+    """The tokens' slots would lie far past the last one (their count passes 32
+    bits): skipped and flagged."""
+    k, v = _kv(10, 2, torch.bfloat16, 7)
+    kc = torch.full((1, 2, 64, 80), 171, dtype=torch.uint8, device="cuda")
+    vc = kc.clone()
+    kb = torch.full((10, 2, D), 3.0, dtype=torch.bfloat16, device="cuda")
+    vb = kb.clone()
+    wb.kv_store_q4(k.cuda(), v.cuda(), kc, vc, _i32([0]), cu_seqlens=_i32([low, 10]))
+    assert wb.device_error(reset=True) == 2
+    wb.kv_load_q4(kc, vc, _i32([0]), kb, vb, cu_seqlens=_i32([low, 10]))
+    assert wb.device_error(reset=True) == 2
+    for c in (kc, vc):
+        assert bool((c == 171).all())
+    for x in (kb, vb):
+        assert bool((x == 3.0).all())
+
+
+def test_a_first_bound_before_the_tokens():
+    """Sequence -2 .. 10: its token 0 is the third one, in slot start + 2."""
+    k, v = _kv(10, 2, torch.bfloat16, 7)
+    kc = torch.full((1, 2, 64, 80), 171, dtype=torch.uint8, device="cuda")
+    vc = kc.clone()
+    wb.kv_store_q4(k.cuda(), v.cuda(), kc, vc, _i32([4]), cu_seqlens=_i32([-2, 10]))
+    assert wb.device_error(reset=True) == 0
+    ref = np.full((1, 2, 64, 80), 171, np.uint8)
+    ref[0, :, 6:16] = sv.quantize_rows(k.float().numpy(), True).transpose(1, 0, 2)
+    assert np.array_equal(kc.cpu().numpy(), ref)

@@ -217,3 +217,61 @@ def test_oracle_logprobs_by_hand():
     assert np.isclose(ent[0], -(np.log(1 / 7) / 7 + 6 / 7 * np.log(3 / 7)))
     assert top.tolist() == [[1, 3, 0], [3, 2, 1]]
     assert np.isnan(ent[1]) and np.isnan(lp[1]).all()
+
+
+def _places_by_definition(cu, rows, start, T, n_rows, S):
+    """Each token's row * S + slot, -1 skipped, -2 flagged, in Python's integers."""
+    got = [-1] * T
+    for i, s0 in enumerate(start):
+        lo, hi = (i, i + 1) if cu is None else (cu[i], cu[i + 1])
+        r = i if rows is None else rows[i]
+        for t in range(max(lo, 0), min(hi, T)):
+            if s0 >= 0:
+                ok = 0 <= r < n_rows and s0 + t - lo < S
+                got[t] = r * S + s0 + t - lo if ok else -2
+    return got
+
+
+@pytest.mark.parametrize("cu,rows,start,S", [
+    ([0, 3, 3, 9], None, [0, 5, 4], 16),
+    ([2, 9], [1], [0], 5),                              # the last two have no slot
+    ([0, 4, 10], [7, -1], [0, 0], 16),                  # rows outside the cache
+    ([0, 4, 10], None, [-1, 2**31 - 1], 16),
+    (None, None, [0] * 5 + [15, 16, -1, -2**31, 2**31 - 1], 16),
+    ([-2147483643, 10], None, [0], 64),                 # hi - lo passes 32 bits
+    ([-2147483648, 10], None, [0], 64),
+    ([-2147483648, 2147483647], None, [0], 64),
+    ([-2147483648, 2147483647], [1], [2147483647], 2147483647),
+    ([-5, 2147483647], [1], [3], 64),
+    ([-3, 6, 2147483647], [1, 0], [2147483640, 0], 2147483647),
+])
+def test_kv_places_whatever_the_bounds(lib, cu, rows, start, S):
+    """The kernels' placement on the CPU: no token gets a slot outside its row,
+    however far the bounds lie outside the tokens."""
+    T, n_rows = 10, 10
+    got = wb.debug_kv_places(cu, rows, start, T, n_rows, S)
+    assert got == _places_by_definition(cu, rows, start, T, n_rows, S)
+
+
+def test_kv_places_of_random_bounds_that_rise(lib):
+    rng = np.random.default_rng(5)
+    edges = [-2**31, -2**31 + 7, -2**30, -100, -1, 0, 1, 5, 17, 40, 41, 2**30, 2**31 - 1]
+    for _ in range(400):
+        n = int(rng.integers(1, 6))
+        cu = sorted(int(x) for x in rng.choice(edges, n + 1))
+        rows = [int(x) for x in rng.integers(-1, 4, n)] if rng.random() < 0.7 else None
+        start = [int(x) for x in rng.choice([-1, 0, 3, 30, 2**31 - 1], n)]
+        S = int(rng.choice([1, 8, 33, 2**31 - 1]))
+        got = wb.debug_kv_places(cu, rows, start, 40, 3, S)
+        assert got == _places_by_definition(cu, rows, start, 40, 3, S), (cu, rows, start, S)
+
+
+def test_kv_places_of_bounds_in_any_order_stay_in_the_cache(lib):
+    """Bounds that fall: tokens may go with another sequence, never past a row."""
+    rng = np.random.default_rng(6)
+    for _ in range(400):
+        n, S = int(rng.integers(1, 6)), int(rng.choice([1, 8, 33]))
+        cu = [int(x) for x in rng.choice([-2**31, -9, 0, 3, 12, 40, 90, 2**31 - 1], n + 1)]
+        start = [int(x) for x in rng.choice([-1, 0, 3, 30], n)]
+        got = wb.debug_kv_places(cu, None, start, 40, 3, S)
+        assert all(-2 <= p < 3 * S for p in got), (cu, start, S)

@@ -160,6 +160,7 @@ _OTHER = {
     "ws_get_tuning": ([P], None),
     "ws_debug_gemv_copies": ([I32, I32, I32, I32, I32, I32, P, C.c_long], C.c_long),
     "ws_debug_gemv_copies_q4": ([I32, I32, I32, I32, I32, I32, P, C.c_long, P], C.c_long),
+    "ws_debug_kv_places": ([P, P, P, I32, I32, I32, I32, P], C.c_long),
     "ws_version": ([], C.c_char_p),
 }
 
@@ -603,6 +604,17 @@ def debug_gemv_copies(M, K, B, nmat, allow_split, cta):
     buf = (C.c_longlong * (3 * max(n, 1)))()
     lib.ws_debug_gemv_copies(M, K, B, nmat, int(allow_split), cta, buf, n)
     return [(buf[3 * i], buf[3 * i + 1], buf[3 * i + 2]) for i in range(n)]
+
+
+def debug_kv_places(cu_seqlens, rows, start, T, n_rows, s_max):
+    """Per token of one head: row * s_max + slot, -1 skipped, -2 flagged (host lists)."""
+    def ints(v):
+        return None if v is None else (C.c_int32 * len(v))(*v)
+    out = (C.c_longlong * T)()
+    if load().ws_debug_kv_places(ints(cu_seqlens), ints(rows), ints(start), T, len(start), n_rows,
+                                 s_max, out) < 0:
+        raise WsError(-1, "bad arguments")
+    return list(out)
 
 
 def version() -> str:

@@ -38,11 +38,15 @@ struct KvPlace {
   int lim;        // those before lim have a slot
   bool over;      // those from lim on lack one that they should have
   size_t at;      // row (of 80 bytes) of token lo
+  __host__ __device__ bool holds(int t) const { return t >= lo && t < hi; }
+  // row of token t < lim (a bound may be as low as an int goes: t - lo in 64 bits)
+  __host__ __device__ size_t row(int t) const { return at + (size_t)((long long)t - lo); }
 };
 
 // The place of the sequence that token t is in (t alone where it is in none).
-// No access is made outside the cache: a row or slot there only sets `over`.
-__device__ __forceinline__ void kv_find(const KvRowsParams& a, int t, int g, KvPlace& p) {
+// No access is made outside the cache, whatever the bounds: a row or slot there
+// only sets `over`.
+__host__ __device__ __forceinline__ void kv_find(const KvRowsParams& a, int t, int g, KvPlace& p) {
   int i = t;
   p = {t, t + 1, t, false, 0};
   if (a.cu) {
@@ -60,7 +64,9 @@ __device__ __forceinline__ void kv_find(const KvRowsParams& a, int t, int g, KvP
   const int s0 = a.start[i], row = a.rows ? a.rows[i] : i;
   if (s0 < 0) return;
   if (row >= 0 && row < a.n_rows && s0 < a.S) {
-    p.lim = p.lo + min(p.hi - p.lo, a.S - s0);
+    // the tokens' count may pass 32 bits, that of the slots does not
+    const long long tokens = (long long)p.hi - p.lo, slots = a.S - s0;
+    p.lim = (int)(p.lo + (tokens < slots ? tokens : slots));
     p.at = ((size_t)row * a.nkv + g) * a.S + s0;
   }
   p.over = p.lim < p.hi;
@@ -95,8 +101,8 @@ __global__ void __launch_bounds__(kKvWarps * 32, 4) k_kv_store_q4(const __grid_c
 #pragma unroll
         for (int e = 0; e < (DT == DT_F32 ? 2 : 1); ++e)
           raw[u][e] = __ldcs(reinterpret_cast<const uint4*>(src + u * kKvWarps * stride) + e);
-        if (t < place.lo || t >= place.hi) kv_find(a, t, g, place);
-        if (t < place.lim) dst[u] = cache + (place.at + (t - place.lo)) * kKvRow;
+        if (!place.holds(t)) kv_find(a, t, g, place);
+        if (t < place.lim) dst[u] = cache + place.row(t) * kKvRow;
         else if (place.over && lane == 0) atomicExch(a.err, kDerrBadSlot);
       }
     }
@@ -134,9 +140,9 @@ __global__ void __launch_bounds__(kKvWarps * 32, 8) k_kv_load_q4(const __grid_co
       const int t = base + (i + u) * kKvWarps;
       there[u] = i + u < a.per && t < a.T;
       if (!there[u]) continue;
-      if (t < place.lo || t >= place.hi) kv_find(a, t, g, place);
+      if (!place.holds(t)) kv_find(a, t, g, place);
       there[u] = t < place.lim;
-      if (there[u]) word[u] = get_word(cache + (place.at + (t - place.lo)) * kKvRow, at);
+      if (there[u]) word[u] = get_word(cache + place.row(t) * kKvRow, at);
       else if (place.over && lane == 0) atomicExch(a.err, kDerrBadSlot);
     }
 #pragma unroll
@@ -251,6 +257,30 @@ ws_status ws_kv_load_q4(const void *k_cache, const void *v_cache, const int32_t 
   a.nkv = n_kv_heads;
   a.S = s_max;
   return kv_rows(a, dtype, head_dim, false, (cudaStream_t)stream);
+}
+
+long ws_debug_kv_places(const int32_t *cu_seqlens, const int32_t *rows, const int32_t *start, int T,
+                        int n_seqs, int n_rows, int s_max, long long *places) {
+  if (!start || !places || T < 1 || n_seqs < 1 || n_rows < 1 || s_max < 1 ||
+      (!cu_seqlens && T != n_seqs))
+    return -1;
+  KvRowsParams a = {};
+  a.cu = cu_seqlens;
+  a.rows = rows;
+  a.start = start;
+  a.T = T;
+  a.n = n_seqs;
+  a.n_rows = n_rows;
+  a.nkv = 1;
+  a.S = s_max;
+  KvPlace place = {0, 0, 0, false, 0};
+  long found = 0;
+  for (int t = 0; t < T; ++t) {
+    if (!place.holds(t)) kv_find(a, t, 0, place);
+    places[t] = t < place.lim ? (long long)place.row(t) : place.over ? -2 : -1;
+    found += t < place.lim;
+  }
+  return found;
 }
 
 }  // extern "C"
