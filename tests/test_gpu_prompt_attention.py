@@ -263,3 +263,47 @@ def test_two_calls_at_once_on_two_streams():
     torch.cuda.synchronize()
     _check(*a, [0, 700], outs[0].cpu(), None)
     _check(*b, [0, 300], outs[1].cpu(), None)
+
+
+def _withheld(q, k, v, bounds, copy, limit_ms=100):
+    """The call with one copy of CTA 0 left out: (out, milliseconds)."""
+    from _util import tuning
+    dev = [x.cuda() for x in (q, k, v)]
+    out = torch.full((q.shape[0], q.shape[1] * D), 7.0, dtype=q.dtype, device="cuda")
+    cu = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    with tuning(timeout_ns=limit_ms * 1_000_000):
+        wb.test_withhold(0, copy)
+        try:
+            a.record()
+            wb.prompt_attention(*dev, cu, out)
+            b.record()
+            torch.cuda.synchronize()
+        finally:
+            wb.test_withhold(-1)
+    return out, a.elapsed_time(b)
+
+
+# CTA 0 is the longest tile: of one block; of six; of the last two runs of 600
+# tokens of one head (blocks 4 and 5 of which tile 1 alone has the last)
+@pytest.mark.parametrize("nh,nkv,n,copies", [(2, 1, 100, [0, 1, 2, 3]), (1, 1, 100, [0, 2, 3]),
+                                             (2, 1, 700, [0, 1, 2, 3, 4, 5, 6, 9, 10, 11, 12, 13]),
+                                             (1, 1, 700, [0, 1, 2, 3, 6, 7, 10, 11, 12, 13])])
+def test_a_copy_that_does_not_come(nh, nkv, n, copies):
+    """The wait for it runs out: error 1, the other CTAs' rows as ever, and the
+    call back after that one limit: what is waited for then are copies and
+    products under way, never the one that was not started (that would take a
+    second limit).  The next call is right."""
+    q, k, v = _inputs(n + 30, nh, nkv, torch.bfloat16, n + nh)
+    bounds = [0, n, n + 30]
+    whole, _ = _call(q, k, v, bounds)
+    _check(q, k, v, bounds, whole, None)
+    rows = 128 if nh == 2 else 256
+    rest = torch.ones(n + 30, dtype=torch.bool)
+    rest[(n - 1) // rows * rows:n] = False  # the longest tile's rows
+    for copy in copies:
+        out, ms = _withheld(q, k, v, bounds, copy)
+        assert wb.device_error(reset=True) == 1, copy
+        assert 99 <= ms < 180, (copy, ms)
+        assert torch.equal(out.cpu()[rest], whole[rest]), copy
+        assert torch.equal(_call(q, k, v, bounds)[0], whole), copy

@@ -140,6 +140,7 @@ _SIGS = {
     "ws_read_probe": [P, SZ, I32, P, P],
     "ws_empty_probe": [I32, P, P, P],
     "ws_test_bounded_wait": [C.c_ulonglong, P],
+    "ws_test_withhold": [I32, I32],
 }
 _OTHER = {
     "ws_workspace_bytes": ([I32, I32, I32, I32], SZ),
@@ -560,6 +561,10 @@ def empty_probe(touch, ptr=None, sink=None, stream=None):
 
 def test_bounded_wait(timeout_ns, stream=None):
     _check(load().ws_test_bounded_wait(int(timeout_ns), _stream(stream)))
+
+
+def test_withhold(cta, copy=0):
+    _check(load().ws_test_withhold(int(cta), int(copy)))
 
 
 def device_error(reset=False) -> int:

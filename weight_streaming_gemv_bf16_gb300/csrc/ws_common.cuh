@@ -297,6 +297,16 @@ struct Tuning {
   int q4_mma;        // 4-bit ops with two 16-row tasks per warp or more on tensor cores: 1 at B 2..4, 2 always
 };
 
+// For the tests of waits that run out: the copy that one CTA of a launch leaves
+// out (ws_test_withhold); no CTA by default.
+struct TestHold {
+  int cta, copy;
+#ifdef __CUDACC__
+  __device__ __forceinline__ int here() const { return (int)blockIdx.x == cta ? copy : -1; }
+#endif
+};
+TestHold& test_hold();
+
 // Host-side helpers implemented in ws_gemv.cu / ws_misc.cu.
 Tuning& tuning();
 int device_sm_count();

@@ -279,6 +279,11 @@ cudaError_t launch_copy_words(void* d0, const void* s0, size_t b0, void* d1, con
                             static_cast<const uint32_t*>(s1), n1);
 }
 
+TestHold& test_hold() {
+  static TestHold hold = {-1, 0};
+  return hold;
+}
+
 size_t argmax_rows_workspace(int rows, int cols) {
   if (rows <= 0 || cols <= 0) return 0;
   const size_t cb = (size_t)argmax_cols_per_row_blocks(cols);
@@ -422,6 +427,15 @@ ws_status ws_test_bounded_wait(unsigned long long timeout_ns, ws_stream_t stream
   }
   k_test_bounded_wait<<<1, 32, 0, (cudaStream_t)stream>>>(timeout_ns, err);
   return launch_status();
+}
+
+ws_status ws_test_withhold(int cta, int copy) {
+  if (cta < -1 || copy < 0) {
+    set_error("cta -1 (none) or an index, copy an index");
+    return WS_ERR_ARG;
+  }
+  test_hold() = {cta, copy};
+  return WS_OK;
 }
 
 }  // extern "C"

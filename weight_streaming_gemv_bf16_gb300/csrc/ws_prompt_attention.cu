@@ -75,13 +75,15 @@ struct PromptParams {
   float scale;             // log2(e) / sqrt(128)
   int* err;
   unsigned long long timeout_ns;
+  TestHold hold;           // copies: 0, 1 the tiles' queries, 2 + 2 j and 3 + 2 j block j's keys and values
 };
 
 struct PaShared {
   uint64_t q_full[2], k_full[kPaStages], k_empty[kPaStages], v_full[kPaStages], v_empty[kPaStages];
-  uint64_t s_full[2], p_full[2][kPaParts], o_full[2], guard_go[2], guard[2], drain[2];
+  uint64_t s_full[2], p_full[2][kPaParts], o_full[2], guard_go[2], guard[2];
   uint32_t tmem;
   uint32_t odd[2][4];      // values of the guarded blocks that are not finite, a bit a key
+  int sent[6];             // copies started on q_full, k_full and v_full, each in turn
   int abort;
 };
 
@@ -233,11 +235,18 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   unsigned char* sk = smem + 2 * kPaTileBytes;
   unsigned char* sv = sk + kPaStages * kPaTileBytes;
 
-  // a tile's rows of one head: two boxes of 64 dimensions
-  auto copy = [&](unsigned char* dst, const CUtensorMap* map, int h, int tok, uint64_t* bar) {
+  // a tile's rows of one head: two boxes of 64 dimensions; `id` as in the
+  // parameters' `hold`, `slot` the barrier's place in `sent`
+  // (asked for once: a comparison of the CTA's index with the parameter ahead of
+  // each copy took 8192 tokens, 32/8 heads from 321 to 333 us)
+  const int hold = a.hold.here();
+  auto copy = [&](unsigned char* dst, const CUtensorMap* map, int h, int tok, uint64_t* bar, int slot,
+                  int id) {
+    if (id == hold) return;
     mbar_arrive_expect_tx(bar, kPaTileBytes);
     tma_load_3d(dst, map, 0, h, tok, bar);
     tma_load_3d(dst + kPaHalf, map, 64, h, tok, bar);
+    ++sh.sent[slot];
   };
   // the copies' warp starts the barriers and the first copies before the
   // tensor memory is there
@@ -249,7 +258,6 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       mbar_init(&sh.o_full[i], 1);
       mbar_init(&sh.guard_go[i], 1);
       mbar_init(&sh.guard[i], 128);
-      mbar_init(&sh.drain[i], 1);
     }
     for (int i = 0; i < kPaStages; ++i) {
       mbar_init(&sh.k_full[i], 1);
@@ -259,10 +267,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     }
     fence_mbar_init();
     sh.abort = 0;
-    copy(sq, &a.mq, h0, first + row0, &sh.q_full[0]);
-    copy(sk, &a.mk, kvh, first, &sh.k_full[0]);
-    if (n1 > 0) copy(sq + kPaTileBytes, &a.mq, h0 + a.pair, first + row1, &sh.q_full[1]);
-    copy(sv, &a.mv, kvh, first, &sh.v_full[0]);
+    for (int i = 0; i < 6; ++i) sh.sent[i] = 0;
+    copy(sq, &a.mq, h0, first + row0, &sh.q_full[0], 0, 0);
+    copy(sk, &a.mk, kvh, first, &sh.k_full[0], 2, 2);
+    if (n1 > 0) copy(sq + kPaTileBytes, &a.mq, h0 + a.pair, first + row1, &sh.q_full[1], 1, 1);
+    copy(sv, &a.mv, kvh, first, &sh.v_full[0], 4, 3);
     if (guard0 == 0) mbar_arrive(&sh.guard_go[0]);
   }
   if (threadIdx.x < 8) sh.odd[threadIdx.x >> 2][threadIdx.x & 3] = 0;
@@ -271,6 +280,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  // every role's end; after it nothing more is issued, and `abort` stays as it is
+  auto leave = [&]() {
+    __syncwarp();
+    tc_fence_before();
+    consumer_sync(kPaThreads);
+  };
+  auto aborted = [&]() { return *(volatile int*)&sh.abort != 0; };
 
   if (warp < 8) {
     regs_raise<kPaRegsSoftmax>();
@@ -358,7 +374,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 #pragma unroll 1
     for (int j = 0; j < n - 1 && ok; ++j) softmax(j, std::false_type());
     if (n > 0 && ok) softmax(n - 1, std::true_type());
-    if (n > 0 && ok) ok = __all_sync(0xffffffffu, pa_wait(&sh.o_full[tile], 0, &sh, a));
+    if (n > 0 && ok) ok = __all_sync(0xffffffffu, pa_wait(&sh.o_full[tile], 0, &sh, a) && !aborted());
     if (n > 0 && ok) {
       tc_fence_after();
       const float sum = l.x + l.y, inv = 1.f / sum;
@@ -399,6 +415,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
               *reinterpret_cast<const uint4*>(st + rr * 256 + (piece ^ (rr & 7)) * 16);
       }
     }
+    leave();
   } else {
     regs_lower<kPaRegsOther>();
     if (warp < 10) {
@@ -445,35 +462,19 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           if (j + 1 < n) scores(j + 1);
           else mma_commit(&sh.o_full[tile]);
         }
-        // after a wait that ran out: nothing of this thread's stays in flight
-        if (!ok) {
-          mma_commit(&sh.drain[tile]);
-          mbar_wait_bounded(&sh.drain[tile], 0, a.timeout_ns);
-        }
+        if (!ok) mma_commit(&sh.o_full[tile]);  // either way: behind every product of the tile
       }
     } else if (warp == 10) {
       if (elect_one()) {
-        bool ok = true;
-        int j = 1;  // block 0 is on its way
-        for (; j < nb; ++j) {
+        for (int j = 1; j < nb; ++j) {  // block 0 is on its way
           const int s = j % kPaStages;
           const uint32_t par = (j / kPaStages + 1) & 1;
-          if (j >= kPaStages) ok = pa_wait(&sh.k_empty[s], par, &sh, a);
-          if (!ok) break;
-          copy(sk + s * kPaTileBytes, &a.mk, kvh, first + j * kPaTile, &sh.k_full[s]);
-          if (j >= kPaStages) ok = pa_wait(&sh.v_empty[s], par, &sh, a);
-          if (!ok) break;
-          copy(sv + s * kPaTileBytes, &a.mv, kvh, first + j * kPaTile, &sh.v_full[s]);
+          if (j >= kPaStages && !pa_wait(&sh.k_empty[s], par, &sh, a)) break;
+          copy(sk + s * kPaTileBytes, &a.mk, kvh, first + j * kPaTile, &sh.k_full[s], 2 + s, 2 + 2 * j);
+          if (j >= kPaStages && !pa_wait(&sh.v_empty[s], par, &sh, a)) break;
+          copy(sv + s * kPaTileBytes, &a.mv, kvh, first + j * kPaTile, &sh.v_full[s], 4 + s, 3 + 2 * j);
           // from here on the stage's phase is this block's
           if (j >= guard0) mbar_arrive(&sh.guard_go[j - guard0]);
-        }
-        if (!ok) {  // the copies that are still under way
-          mbar_wait_bounded(&sh.q_full[0], 0, a.timeout_ns);
-          if (n1 > 0) mbar_wait_bounded(&sh.q_full[1], 0, a.timeout_ns);
-          for (int i = max(0, j - kPaStages); i <= j; ++i) {
-            if (i < j || i == nb) mbar_wait_bounded(&sh.v_full[i % kPaStages], (i / kPaStages) & 1, a.timeout_ns);
-            mbar_wait_bounded(&sh.k_full[i % kPaStages], (i / kPaStages) & 1, a.timeout_ns);
-          }
         }
       }
     } else if (warp >= 12) {
@@ -510,10 +511,21 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         mbar_arrive(&sh.guard[j - guard0]);
       }
     }
+    leave();
+    // After a wait that ran out, whoever's it was: no product and no copy of this
+    // CTA stays under way behind it.
+    if (warp < 10 && aborted()) {
+      if (warp == 8 || n1 > 0) mbar_wait_bounded(&sh.o_full[warp - 8], 0, a.timeout_ns);
+    } else if (warp == 10 && aborted()) {
+      static_assert(kPaStages == 2, "six barriers of copies");
+      if (elect_one())
+        for (int i = 0; i < 6; ++i) {
+          uint64_t* bar = i < 2 ? &sh.q_full[i] : i < 4 ? &sh.k_full[i - 2] : &sh.v_full[i - 4];
+          if (sh.sent[i]) mbar_wait_bounded(bar, (sh.sent[i] - 1) & 1, a.timeout_ns);
+        }
+    }
   }
-  __syncwarp();
-  tc_fence_before();
-  __syncthreads();
+  if (aborted()) __syncthreads();
   if (warp == 8) {
     tc_fence_after();
     tmem_free(tmem, 512);
@@ -637,6 +649,7 @@ ws_status ws_prompt_attention(const void *q, const void *k, const void *v, int d
   a.nkv = n_kv_heads;
   a.scale = (float)(1.4426950408889634 / sqrt((double)kPromptDim));
   a.timeout_ns = tuning().timeout_ns;
+  a.hold = test_hold();
   a.err = device_error_ptr();
   if (!a.err) {
     set_error("device error flag unavailable");
