@@ -319,9 +319,11 @@ ws_status ws_decode_attention_q4(const float *q, const float *k_new, const float
  * or +infinity, or nothing but -infinity, has NaN log-probabilities and
  * entropy; its alternatives are still ordered, a NaN never among them (places
  * left over: index -1, NaN).
+ * A row in which a wait ran out (device error 1) has NaN for every value.
  * Workspace (zero-filled before its first use, left ready for the next call
- * by every call): ws_logprobs_workspace_bytes(rows, V, topk), 0 for sizes
- * that the call refuses; calls that share one must not overlap. */
+ * by every call, one with such a row too): ws_logprobs_workspace_bytes(rows, V,
+ * topk), 0 for sizes that the call refuses; calls that share one must not
+ * overlap. */
 size_t ws_logprobs_workspace_bytes(int rows, int V, int topk);
 ws_status ws_token_logprobs(const void *logits, int dtype, long long ld, const int32_t *targets,
                             float *logprob, float *entropy, int32_t *top_idx, float *top_logprob,
@@ -719,10 +721,11 @@ ws_status ws_empty_probe(int touch, const uint32_t *ptr, uint32_t *sink, ws_stre
  * arrives on, for timeout_ns, then records the time-out in the device error
  * flag and returns. */
 ws_status ws_test_bounded_wait(unsigned long long timeout_ns, ws_stream_t stream);
-/* Test hook for the waits inside ws_prompt_attention: in launches from here on
- * the CTA with index `cta` leaves out one copy, so that the wait for it runs
- * out (copies 0 and 1 are the queries of its two tiles, 2 + 2 j and 3 + 2 j the
- * keys and values of its block j); cta -1, the default: none. */
+/* Test hook for the waits inside ws_prompt_attention and ws_token_logprobs: in
+ * launches from here on the CTA with index `cta` leaves out one copy, so that
+ * the wait for it runs out (prompt attention: copies 0 and 1 are the queries of
+ * its two tiles, 2 + 2 j and 3 + 2 j the keys and values of its block j;
+ * log-probabilities: copy j is its step j); cta -1, the default: none. */
 ws_status ws_test_withhold(int cta, int copy);
 
 const char *ws_version(void);

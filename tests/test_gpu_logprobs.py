@@ -267,3 +267,43 @@ def test_row_counts_around_the_cuts_on_one_workspace(k):
         x = _logits(n, V, torch.bfloat16, n)
         t = _targets(n, V, n)
         _check(x, k, t, _call(x.cuda(), k, t, ws=ws))
+
+
+@pytest.mark.parametrize("rows,V,cta,copy", [(2, 151936, 1, 0), (2, 151936, 0, 0), (3, 300000, 50, 1),
+                                             (1300, 9001, 7, 0), (1300, 9001, 7, 1), (1300, 9001, 7, 2)])
+@pytest.mark.parametrize("k", [0, 5, 20])
+def test_a_copy_that_does_not_come(rows, V, cta, copy, k):
+    """The wait for it runs out: error 1, that row NaN, the others as ever, back
+    after one limit; and the workspace serves the next calls."""
+    from _util import tuning
+    dtype = torch.bfloat16 if rows > 100 else torch.float32
+    limit_ms = 100
+    ws = torch.zeros(wb.logprobs_workspace_bytes(rows, V, k), dtype=torch.uint8, device="cuda")
+    x, t = _logits(rows, V, dtype, 1), _targets(rows, V, 1)
+    whole = _call(x.cuda(), k, t, ws=ws)
+    y = _logits(rows, V, dtype, 2)
+    other = _call(y.cuda(), k, t, ws=ws)
+    dev = x.cuda()
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    with tuning(timeout_ns=limit_ms * 1_000_000):
+        wb.test_withhold(cta, copy)
+        try:
+            a.record()
+            got = _call(dev, k, t, ws=ws)
+            b.record()
+            torch.cuda.synchronize()
+        finally:
+            wb.test_withhold(-1)
+    assert wb.device_error(reset=True) == 1
+    assert limit_ms - 1 <= a.elapsed_time(b) < 1.8 * limit_ms
+    bad = 0 if V == 151936 else 1 if V == 300000 else cta
+    rest = np.arange(rows) != bad
+    for n in whole:
+        assert np.array_equal(got[n][rest], whole[n][rest]), n
+        if n != "top_idx":
+            assert np.isnan(got[n][bad]).all(), n
+    for _ in range(2):
+        again = _call(y.cuda(), k, t, ws=ws)
+        assert all(np.array_equal(again[n], other[n]) for n in other)
+        again = _call(dev, k, t, ws=ws)
+        assert all(np.array_equal(again[n], whole[n]) for n in whole)

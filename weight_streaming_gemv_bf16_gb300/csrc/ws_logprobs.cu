@@ -50,6 +50,7 @@ struct LogprobParams {
   unsigned long long* keys;    // [rows][splits][k]
   int* err;
   unsigned long long timeout_ns;
+  TestHold hold;               // copies: the CTA's steps
 };
 
 // A key that orders as (value, lower index): the value's bits made monotone,
@@ -310,7 +311,9 @@ __global__ void __launch_bounds__(kLpThreads, 8) k_token_logprobs(const __grid_c
   constexpr uint32_t kNegInf = DT == DT_F32 ? 0xff800000u : DT == DT_BF16 ? 0xff80ff80u : 0xfc00fc00u;
   constexpr int kStepVec = kLpThreads * kLoads, kStepBytes = kStepVec * 16;
   const int steps = (nv + kStepVec - 1) / kStepVec;
+  const int hold = a.hold.here();
   auto fill = [&](int step) {  // one thread
+    if (step == hold) return;
     const int bytes = min(kStepBytes, (nv - step * kStepVec) * 16);
     uint64_t* bar = &sh.full[step % kLpStages];
     mbar_arrive_expect_tx(bar, bytes);
@@ -404,7 +407,7 @@ __global__ void __launch_bounds__(kLpThreads, 8) k_token_logprobs(const __grid_c
     // one barrier a step: the stage is free again, and whether the candidates
     // are many (more than there is room for: their best raise the bound, and
     // the step's values are gone through again) or a wait ran out
-    bool again = false;
+    bool again = false, lost = false;
     do {
       if (TOP && mx >= thrv) {
         const uint32_t packed = LpRegs<DT>::pack_down(thrv);
@@ -426,12 +429,17 @@ __global__ void __launch_bounds__(kLpThreads, 8) k_token_logprobs(const __grid_c
       again = false;
       if (__syncthreads_or(!ok || (TOP && over >= kLpCompact))) {
         if (sh.abort) {
+          // the row comes out as NaN; this part of it has no candidates, and its
+          // ticket is taken below as ever
           if (t == 0) {
             atomicExch(a.err, (int)DERR_TIMEOUT);
             for (int i = step; i < steps && i < step + kLpStages; ++i)  // copies under way
-              mbar_wait_bounded(&sh.full[i % kLpStages], (i / kLpStages) & 1, a.timeout_ns);
+              if (i != hold) mbar_wait_bounded(&sh.full[i % kLpStages], (i / kLpStages) & 1, a.timeout_ns);
+            sh.n = 0;
           }
-          return;
+          s.z = s.t = NAN;
+          lost = true;
+          break;
         }
         if (TOP) {
           const int n = sh.n;
@@ -444,6 +452,7 @@ __global__ void __launch_bounds__(kLpThreads, 8) k_token_logprobs(const __grid_c
         }
       }
     } while (TOP && again);
+    if (lost) break;
     if (t == 0 && step + kLpStages < steps) {
       fence_proxy_async_smem();  // the reads of this stage before the copy into it
       fill(step + kLpStages);
@@ -626,6 +635,7 @@ ws_status ws_token_logprobs(const void *logits, int dtype, long long ld, const i
   LogprobParams a = {};
   a.x = logits;
   a.timeout_ns = tuning().timeout_ns;
+  a.hold = test_hold();
   a.targets = targets;
   a.logprob = logprob;
   a.entropy = entropy;
