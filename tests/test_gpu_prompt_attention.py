@@ -307,3 +307,28 @@ def test_a_copy_that_does_not_come(nh, nkv, n, copies):
         assert 99 <= ms < 180, (copy, ms)
         assert torch.equal(out.cpu()[rest], whole[rest]), copy
         assert torch.equal(_call(q, k, v, bounds)[0], whole), copy
+
+
+@pytest.mark.parametrize("nh,nkv", [(2, 1), (1, 1)])
+@pytest.mark.parametrize("first", [0, 70, 200])
+def test_scores_far_below_zero(first, nh, nkv):
+    """Finite scores of -6e34 and less: one key's is the largest by far, so its
+    probability is 1, the others' 0, and the output that key's value to the bit;
+    a token before it, and the only token of a sequence, take theirs likewise.
+    Every score is a power of two's multiple, exact in fp32; the log-sum-exp is
+    the score, off by four roundings."""
+    T = 300
+    _, _, v = _inputs(T + 1, nh, nkv, torch.bfloat16, first)
+    q = torch.full((T + 1, nh, D), 2.0 ** 56, dtype=torch.bfloat16)
+    k = torch.full((T + 1, nkv, D), -(2.0 ** 58), dtype=torch.bfloat16)
+    k[:first] = -(2.0 ** 60) * (1 + torch.arange(first) % 128 / 128)[:, None, None].bfloat16()
+    k[first] = -(2.0 ** 56)
+    bounds = [0, T, T + 1]
+    out, lse = _call(q, k, v, bounds)
+    out = out.view(T + 1, nh, D)
+    for h in range(nh):
+        assert torch.equal(out[first:T, h], v[first, 0].expand(T - first, D))
+        assert torch.equal(out[T, h], v[T, 0]) and torch.equal(out[0, h], v[0, 0])
+    ref = -128 * 2.0 ** 112 / np.sqrt(D)
+    assert np.abs(lse[first:T] / ref - 1).max() <= 2.0 ** -22
+    assert np.abs(lse[T] / (4 * ref) - 1).max() <= 2.0 ** -22

@@ -33,6 +33,7 @@
 // maxima with the loads (tcgen05.ld.red) and the two-part hand-over the rest.
 // Prompts that fill less than one wave take as long as their longest tile's
 // chain, with about 4.6 us before and behind it.
+#include <cfloat>
 #include <cmath>
 #include <mutex>
 #include <type_traits>
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     const int tok = (tile ? row1 : row0) + r;  // of the sequence
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + tile * 128 + lanes, to = tmem + 256 + tile * 128 + lanes;
-    float m = -1e30f;
+    float m = -FLT_MAX;  // below every finite score
     float2 l = make_float2(0.f, 0.f);
     bool ok = true;
     // one block of keys; the last one holds the diagonal
