@@ -306,3 +306,25 @@ def test_offsets_past_four_gigabytes():
     wb.decode_attention_q4(q, kn, vn, kc, vc, p, _ws(2, 4, 4, S), out_f32=o)
     torch.cuda.synchronize()
     _compare(*host, [n - 1] * 2, o, None, kc[:, :, :n], vc[:, :, :n])
+
+
+@pytest.mark.parametrize("nh", [4, 6])
+@pytest.mark.parametrize("n,best", [(1, 0), (40, 0), (40, 39), (200, 70), (9000, 5000), (9000, 8999)])
+def test_scores_far_below_zero(n, best, nh):
+    """Finite scores of -6e34 and less: one slot's is the largest by far, so its
+    probability is 1, the others' 0, and the output the value that its row stands
+    for, to the bit (the part of the codes is exact, the zero joins in one
+    rounding, as in the load)."""
+    host = list(_inputs(1, nh, 1, n, [n - 1], n + best))
+    host[0][:] = 2.0 ** 56
+    k = np.full((1, n, D), -(2.0 ** 58), np.float32)
+    k[0, best] = -(2.0 ** 56)
+    host[3][0, :, :n - 1] = sv.quantize_rows(k[:, :n - 1], True)
+    host[1][:] = k[0, n - 1]
+    q, kn, vn, kc, vc = _dev(*host)
+    o = torch.full((1, nh * D), 7.0, device="cuda")
+    p = torch.tensor([n - 1], dtype=torch.int32, device="cuda")
+    wb.decode_attention_q4(q, kn, vn, kc, vc, p, _ws(1, nh, 1, n), out_f32=o)
+    torch.cuda.synchronize()
+    ref = sv.dequantize_rows(vc[0, 0, best].cpu().numpy(), False)
+    assert np.array_equal(o.cpu().numpy().reshape(nh, D), np.broadcast_to(ref, (nh, D)))

@@ -30,6 +30,7 @@
 // the sums came out exact; mixing the two product types cost more than the
 // conversions) 90; nibbles as raw subnormal bf16 operands 72; four stages or
 // three, 8 warps a CTA, 4 CTAs a SM.
+#include <cfloat>
 #include <cmath>
 #include <mutex>
 
@@ -50,7 +51,8 @@ constexpr int kQ4MaxCtas = 1024;
 constexpr int kQ4Merge = 16;                         // partial results merged in one go
 constexpr int kQ4Part = kKvDim + 4;                  // one partial result: acc[128], max, sum, two unused
 constexpr int kQ4Ring = kQ4Warps * kQ4Stages * kQ4StageBytes;
-// the running maximum follows the tile's only when that is 2^8 above it
+// the running maximum follows the tile's only when that is 2^8 above it; it
+// starts at the lowest number, below every finite score
 constexpr float kQ4Lazy = 8.f;
 
 struct AttnQ4Params {
@@ -192,7 +194,7 @@ __device__ __noinline__ void q4_stage_last(const AttnQ4Params& a, size_t seg, in
 __device__ __forceinline__ void q4_merge(const float* first, const float* rest, size_t step, int n,
                                          int h, int lane, float4& O, float& M, float& L) {
   O = make_float4(0.f, 0.f, 0.f, 0.f);
-  M = -1e30f;
+  M = -FLT_MAX;
   L = 0.f;
   for (int i0 = 0; i0 < n; i0 += kQ4Merge) {
     float4 x[kQ4Merge];
@@ -299,7 +301,7 @@ struct Q4Wide {
       q4_split(z.x, z.y, qz[0], qz[1]);
     }
     zmask = rt < 2 ? 0xffffffffu : 0u;
-    m = -1e30f;
+    m = -FLT_MAX;
     l = make_float2(0.f, 0.f);
 #pragma unroll
     for (int e = 0; e < 4; ++e) zo[e] = 0.f;
@@ -495,7 +497,7 @@ struct Q4Narrow {
              hi, lo);
     qz = rg < 4 ? hi : lo;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) m[e] = -1e30f, l[e] = 0.f;
+    for (int e = 0; e < 2; ++e) m[e] = -FLT_MAX, l[e] = 0.f;
 #pragma unroll
     for (int g = 0; g < 4; ++g) zo[g][0] = zo[g][1] = 0.f;
 #pragma unroll
