@@ -183,6 +183,19 @@ def test_binding_refuses_tensors_off_the_current_device_or_misshapen(lib, monkey
                           top_logprob=torch.zeros(2, 5))
 
 
+def test_binding_refuses_a_workspace_in_pieces(monkeypatch):
+    """The size that crosses the ABI is that of one piece: a view whose bytes do
+    not lie behind one another (or are one byte many times) is refused."""
+    monkeypatch.setattr(wb, "_here", lambda: -1)
+    f, st = torch.zeros(2, 512), torch.zeros(2, dtype=torch.int32)
+    n, kc = torch.zeros(2, 256), torch.zeros(2, 2, 10, 80, dtype=torch.uint8)
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 24), torch.zeros(1 << 12)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            wb.decode_attention_q4(f, n, n, kc, kc, st, ws, out_f32=f)
+        with pytest.raises(ValueError, match="workspace"):
+            wb.token_logprobs(f, ws, entropy=torch.zeros(2))
+
+
 @pytest.mark.parametrize("keys", [True, False])
 def test_oracle_rows_are_within_half_a_step(keys):
     """Each value is off by at most half a step, the rounding of the zero (a

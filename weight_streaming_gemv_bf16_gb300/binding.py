@@ -407,7 +407,10 @@ def _stream_on(stream, dev: int):
 
 
 def _space_at(ws, dev: int):
-    _need(ws.get_device() == dev, f"workspace on {ws.device}: expected the current device")
+    if ws.get_device() != dev:
+        raise ValueError(f"workspace on {ws.device}: expected the current device")
+    if not ws.is_contiguous():
+        raise ValueError(f"workspace: expected one piece, got strides {ws.stride()}")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
