@@ -241,3 +241,32 @@ def test_a_first_bound_before_the_tokens():
     ref = np.full((1, 2, 64, 80), 171, np.uint8)
     ref[0, :, 6:16] = sv.quantize_rows(k.float().numpy(), True).transpose(1, 0, 2)
     assert np.array_equal(kc.cpu().numpy(), ref)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("lens,first,behind", [
+    ([700, 0, 1001, 3, 129, 1290, 1, 64, 900, 7], 5, 400),    # 4500 tokens of 4 heads
+    ([4500], 0, 0), ([1] * 60 + [4000, 0, 0, 333], 107, 0),
+])
+def test_many_tokens_a_warp(lens, first, behind, dtype):
+    """Above 16384 tokens and heads a warp takes 16 tokens, eight apart, and keeps a
+    sequence's place between them: ends at every offset, sequences without a row,
+    rows past the last slot, tokens of no sequence."""
+    n, T = len(lens), first + sum(lens) + behind
+    bounds = (first + np.concatenate([[0], np.cumsum(lens)])).tolist()
+    k, v = _kv(T, 4, dtype, T)
+    start = [(11 * i) % 20 for i in range(n)]
+    rows = list(range(n))[::-1]
+    _roundtrip(k, v, bounds, rows, start, n, 5000)
+    if n > 4:
+        start[0], start[4] = -1, 4950   # no sequence; 79 of 129 tokens past the end
+        rows[8 if n == 10 else 2] = n   # a row outside the cache
+        _roundtrip(k, v, bounds, rows, start, n, 5000, flag=2)
+
+
+@pytest.mark.parametrize("T,nkv", [(16384, 1), (16385, 1), (4096, 4), (4097, 4), (2341, 7)])
+def test_token_counts_around_the_change_of_form(T, nkv):
+    k, v = _kv(T, nkv, torch.bfloat16, T)
+    _roundtrip(k, v, [0, T // 3, T], None, [0, 9], 2, T)
+    if T < 5000:
+        _roundtrip(k, v, None, None, [t % 2 for t in range(T)], T, 2)

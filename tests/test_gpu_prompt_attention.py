@@ -332,3 +332,15 @@ def test_scores_far_below_zero(first, nh, nkv):
     ref = -128 * 2.0 ** 112 / np.sqrt(D)
     assert np.abs(lse[first:T] / ref - 1).max() <= 2.0 ** -22
     assert np.abs(lse[T] / (4 * ref) - 1).max() <= 2.0 ** -22
+
+
+@pytest.mark.parametrize("nh,nkv", [(4, 2), (3, 1)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_many_sequences_of_several_tiles(nh, nkv, dtype):
+    """More than 32 sequences, some of several tiles, before and behind the 32nd."""
+    r = np.random.default_rng(45)
+    lens = r.choice([0, 1, 64, 128, 129, 300], 45).tolist()
+    lens[3], lens[31], lens[32], lens[33], lens[44] = 513, 257, 640, 0, 385
+    bounds = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    q, k, v = _inputs(bounds[-1] + 9, nh, nkv, dtype, nh)
+    _check(q, k, v, bounds, *_call(q, k, v, bounds))
