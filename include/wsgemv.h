@@ -227,12 +227,15 @@ ws_status ws_decode_attention(const float *q, const float *k_new, const float *v
  * cu_seqlens: int32 [n_seqs + 1] in device memory, read when the kernel runs:
  * sequence i is the tokens cu_seqlens[i] .. cu_seqlens[i + 1] - 1 (none where
  * the two are equal).  A sequence whose bounds are out of order or outside
- * 0 .. T is skipped and raises the device error flag (3).  out [T][n_heads *
- * 128] of the same type; lse fp32 [T][n_heads], the natural logarithm of each
- * row's sum of e^score, or NULL.  Rows of out and lse outside every sequence
- * are left as they were, and what q, k and v hold there is not used; a value
- * that is not finite reaches only the tokens that attend to it.
- * head_dim must be 128, n_heads a multiple of n_kv_heads; the four matrices
+ * 0 .. T is skipped and raises the device error flag (3); where falling bounds
+ * make other sequences share tokens, rows of those may be left out too.  out
+ * [T][n_heads * 128] of the same type; lse fp32 [T][n_heads], the natural
+ * logarithm of each row's sum of e^score, or NULL.  Rows of out and lse outside
+ * every sequence are left as they were, and what q, k and v hold there is not
+ * used; a value that is not finite reaches only the tokens that attend to it
+ * (an infinite one as NaN where its probability is 0 in q's type).
+ * T and n_seqs at least 1 (a step without tokens is refused: do not make the
+ * call), head_dim 128, n_heads (to 65535) a multiple of n_kv_heads; the four matrices
  * 16-byte aligned, strides a multiple of 8 and at least the heads'
  * dimensions.  The probabilities enter the second product in q's type,
  * everything else is held in fp32. */
@@ -269,9 +272,8 @@ ws_status ws_prompt_attention(const void *q, const void *k, const void *v, int d
  * ws_kv_load_q4: the reverse, with the same arguments: the values that the
  * rows stand for, rounded once to dtype, to k and v contiguous [T][n_kv_heads]
  * [128]; skipped tokens are left as they were.
- * head_dim must be 128, n_kv_heads at most 65535, T at most 2^30, strides a
- * multiple of 8,
- * every matrix 16-byte aligned.  ws_kv_q4_row_bytes: 80, or 0 for another
+ * T (to 2^30), n_seqs, n_rows and s_max at least 1, head_dim 128, n_kv_heads at
+ * most 65535, strides a multiple of 8, every matrix 16-byte aligned.  ws_kv_q4_row_bytes: 80, or 0 for another
  * head_dim. */
 size_t ws_kv_q4_row_bytes(int head_dim);
 ws_status ws_kv_store_q4(const void *k, const void *v, int dtype, const int32_t *cu_seqlens,
@@ -628,8 +630,8 @@ const char *ws_last_error(void);
 
 /* Device error flag of the current device: 1 after a bounded wait ran out, 2
  * after a position or slot outside its cache, 3 after sequence bounds out of
- * order or range, 4 after a token outside the vocabulary; reset != 0 clears it.  Synchronises the device.  Returns -1 if the
- * flag cannot be read. */
+ * order or range, 4 after a token outside the vocabulary; reset != 0 clears it.
+ * Synchronises the device.  Returns -1 if the flag cannot be read. */
 int ws_device_error(int reset);
 
 typedef struct {
@@ -655,7 +657,9 @@ typedef struct {
                           (every kernel here waits for the previous grid
                           before reading its activations; its weights and γ
                           it reads before, so they must not be outputs of
-                          the GEMV launched just before it).  Default 0.     */
+                          the GEMV launched just before it, nor of the kernel
+                          before a serving operator launched just before
+                          it).  Default 0.                                   */
   int mma;             /* 1: launches of a chain form (with forms = 1) with
                           at least 8 Mi weights at batch 5..16 run a warp-
                           level tensor-core kernel (bf16 m16n8k16 MMA, fp32

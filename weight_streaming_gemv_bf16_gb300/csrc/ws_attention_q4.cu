@@ -18,10 +18,15 @@
 // those groups merge.  A warp streams its tiles through a ring of two stages
 // (two bulk copies of 2560 bytes each).
 //
-// Bound by instruction issue, not by DRAM: expanding 4 bits to operands and
-// carrying the scales takes about 800 instructions a warp and tile.  16 rows x
-// 16384 slots x 8 heads (32 query heads; 257 MB): 61.7 us, 4.2 TB/s, 0.62 of the
-// measured copy rate.  What it took from 113 us: nibbles masked in place and
+// Bound by latency, with no unit full: expanding 4 bits to operands and carrying
+// the scales takes about 800 instructions a warp and tile, each chain of them
+// waits for its own, and registers leave 12 warps a SM (8 with 5 to 8 heads a
+// group).  16 rows x 16384 slots x 8 heads (32 query heads; 257 MB): 59.9 us,
+// 4.3 TB/s, 0.63 of the measured copy rate, issue 53% active, integer pipe 49%,
+// DRAM 51%, tensor pipe 20%; with 64 query heads (the core for 8) 74.4 us, 3.5
+// TB/s; 2 rows of 23462 and 11731 slots, 4 heads, 20.4 us with 32 query heads,
+// 18.0 with 16.  What it took from 113 us (these and the figures below with the
+// new rows read back, 1.4 us): nibbles masked in place and
 // raised by one packed fma (no shift for every second one) 93 -> 80; products
 // that start from nothing and two CTAs a SM without spills -> 73; for up to 4
 // heads the operands changed over -> 67; lo terms by the mixed fma -> 63.4; runs
@@ -66,7 +71,7 @@ struct AttnQ4Params {
   uint16_t* out_bf16;
   int B, nh, nkv, S, G;
   float scale;         // log2(e) / sqrt(128)
-  float* part;         // [CTAs][2][G][130]
+  float* part;         // [CTAs][2][G][kQ4Part]
   unsigned* tick;      // [3][kQ4MaxCtas]
   int* err;
   unsigned long long timeout_ns;

@@ -6,10 +6,12 @@
 // writes 160.  A warp takes a token and head at a time, lanes 0..15 its key row
 // and 16..31 its value row, eight dimensions a lane, so that a group of 32 is a
 // quad: its minimum and maximum are two shuffles away and nothing passes
-// through shared memory.  The store is held up by its instructions (154 a row
-// pair, 81 us for 56195 tokens x 8 heads in bf16, 3.6 TB/s), the load by the
-// latency of its reads (60 us, 5.0 TB/s).  A CTA's warps take consecutive tokens of one head:
-// their rows are neighbours in the cache.
+// through shared memory.  For 56195 tokens x 8 heads in bf16 the store takes 77
+// us, 3.9 TB/s: 154 instructions a row pair and their latencies (issue 66%
+// active, integer pipe 55%, DRAM 40%); the load 62-64 us, 4.7 TB/s: the latency of
+// its reads, two of 2 bytes and one of 4 a lane.  fp32: 119 and 130 us, 4.5 and 4.1
+// TB/s.  A CTA's warps take consecutive tokens of one head: their rows are
+// neighbours in the cache.
 #include "ws_kv_q4.cuh"
 
 #include "wsgemv.h"

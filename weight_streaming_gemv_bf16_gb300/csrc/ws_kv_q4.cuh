@@ -1,6 +1,7 @@
 // ws_kv_q4.cuh -- the 4-bit key-value row: its layout and its quantiser,
 // shared by the row store and load (ws_kv_q4.cu) and the decode attention
-// over such a cache (ws_attention_q4.cu).
+// over such a cache (ws_attention_q4.cu); and what all serving kernels share:
+// their launch, packed fp32 arithmetic, 8 values a lane and the error codes.
 //
 // A row is one slot of one key-value head: 128 values in four groups of 32
 // consecutive dimensions, each with a bf16 scale s and zero z; code q (0..15)

@@ -5,9 +5,14 @@
 // entropy -sum p log p = log Z - sum e^(x - m) (x - m) / Z.  One pass, a running
 // maximum per thread (2^x by the special-function unit, which takes x log2 e).
 //
-// Bound by instruction issue, then DRAM: 2048 rows x 151665 bf16 with 20
-// alternatives: 150 us, 4.14 TB/s, 0.61 of the measured copy rate; the sums
-// alone are 6 instructions a value, the search about as much again.  A small
+// Bound by the latencies of its instructions and the barrier of each step, with
+// no unit full: 2048 rows x 151665 bf16 with 20 alternatives: 150 us, 4.14 TB/s,
+// 0.61 of the measured copy rate, issue 61% active, integer pipe 50%, DRAM 51%;
+// the sums alone are 6 instructions a value, the search about as much again (1300
+// rows: 64 us without it, 0.91 of the copy rate; 117 with it).  Shorter rows pay
+// for the search's start and end, in which no copy is under way: 700 x 50257, 23.2
+// us without, 42.1 with 20 alternatives, the floor 10.4; 5000 x 8000, 23.6 and 46.0
+// against 11.8; 558 x 75974, 21.9 and 39.9 against 12.5.  A small
 // batch's rows are cut into steps over up to 48 CTAs, the last of which merges:
 // 16 x 151936 fp32 11.9 us, 1 x 50257 10.7 us, all of it latency (a CTA a row:
 // 196 and 207 us).
@@ -290,9 +295,13 @@ __device__ __noinline__ void lp_compact(LpShared& sh, int n, int k) {
 // every 1, 2, 4, 8 steps: 163, 160, 157, 157 us against 150 for the 2048 rows;
 // the clamp on pairs of 16 bits 156; the search in two levels 150).  The best `k` are found in the same pass:
 // the k-th of the threads' largest values of the first step bounds the k-th of
-// all from below, so that only the few values from there on become candidates;
-// their best ones raise the bound when there are many, which an order that
-// keeps rising makes slower but not wrong.
+// all from below, so that only the values from there on become candidates, few
+// in most rows; their best ones raise the bound when there are many.  An order
+// that keeps rising makes that slower but not wrong, and so does a row in which
+// fewer than k of those largest values are above -infinity: every value ruled out
+// then reaches the bound and is looked at by its index (2048 x 151936 bf16, 20
+// alternatives: 149 us, with 1504 tokens allowed 157, with 18 allowed 479; 16 rows
+// fp32 with 16 allowed 26 against 12).
 template <int DT, bool TOP>
 __global__ void __launch_bounds__(kLpThreads, 8) k_token_logprobs(const __grid_constant__ LogprobParams a) {
   extern __shared__ __align__(128) unsigned char smem[];

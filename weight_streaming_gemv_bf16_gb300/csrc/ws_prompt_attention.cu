@@ -27,12 +27,14 @@
 // Bound by the tensor cores, then by the chain score -> maximum -> powers ->
 // product that each tile goes through (about 2200 cycles a block, 1054 of them
 // in the products; two tiles a CTA overlap to 2700): one sequence of 8192
-// tokens, 32 heads over 8: 328 us, 1676 TFLOP/s of the unmasked pairs, 0.90 of
-// the measured matrix rate; 349 us back to back under the power cap.  A thread
+// tokens, 32 heads over 8: 320-335 us in runs of 30, 1640-1720 TFLOP/s of the
+// unmasked pairs, 0.88-0.92 of the measured matrix rate; 346-358 us in long runs
+// of calls, under the power cap.  A thread
 // for each tile's products instead of one for both took 434 us to 341; row
 // maxima with the loads (tcgen05.ld.red) and the two-part hand-over the rest.
 // Prompts that fill less than one wave take as long as their longest tile's
-// chain, with about 4.6 us before and behind it.
+// chain, about 1.4 us a block, with about 4.6 us before and behind it (1712 + 61
+// tokens, 8/8 heads: 25.6 us, the floor 3.2; 2692 + 129 + 19: 36.4 against 8.0).
 #include <cfloat>
 #include <cmath>
 #include <mutex>
@@ -118,7 +120,9 @@ __device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, PaShared
 
 // Sequence and query block of tile `t` (units of `rows` tokens), by the whole
 // warp: the tiles with the most keys first, whatever their sequence, while the
-// bounds fit the lanes; sequence by sequence beyond that.  false: no such tile.
+// bounds fit the lanes; sequence by sequence beyond that (33 sequences of 20 to
+// 700 tokens, 16/4 heads, 66.4 us, 63.9 when the longest sequences come first; 64
+// of them 110.6 and 107.5).  false: no such tile.
 __device__ __forceinline__ bool pa_place(const PromptParams& a, int t, int rows, int& first,
                                          int& len, int& block) {
   const int lane = threadIdx.x & 31;
