@@ -217,6 +217,8 @@ ws_status ws_decode_attention(const float *q, const float *k_new, const float *v
  * which may begin its setup while the kernel before it on the stream drains and
  * waits for that kernel ahead of its first access to memory.  The first call of
  * each on a device sets its kernels up: make it before any stream capture.
+ * Of a call that raised device error 1 (a wait that ran out) only the workspace
+ * is as ever; its outputs, and rows that it was to append, are not to be used.
  *
  * Causal attention over packed prompts: token t of a sequence attends to that
  * sequence's tokens up to and including t.  Query head h reads key-value head
