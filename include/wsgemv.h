@@ -423,7 +423,8 @@ ws_status ws_kv_store_paged(const void *k, const void *v, int src_dtype, const i
  * bytes (a multiple of 16, to 2^30), one table for all layers; any type that is laid out
  * page by page (bf16, fp16, the 4-bit rows of ws_kv_store_q4).  refs, pages and
  * workspace 16-byte aligned.  Workspace (zero-filled before its first use, left ready
- * by every call): ws_kv_pages_workspace_bytes(n_rows, n_pages); calls that share one, or a table, must
+ * by every call): ws_kv_pages_workspace_bytes(n_rows, n_pages); one that is large enough
+ * serves caches of several sizes in turn; calls that share one, or a table, must
  * not overlap. */
 size_t ws_kv_pages_workspace_bytes(int n_rows, int n_pages);
 ws_status ws_kv_pages_resize(int32_t *table, int32_t *refs, int32_t *tokens, const int32_t *want,

@@ -123,7 +123,7 @@ struct PagesParams {
   long long page_bytes;
   // workspace
   int* head;    // [16]: moves, live pages
-  int* claim;   // [n_rows], zero between calls
+  int* claim;   // [n_rows], zero after a call; what lies behind it depends on n_rows
   int4* rec;    // fork: [n] source row, new row, tokens (-1: skipped), fresh page (-1: none)
   int* list;    // [n_pages] free pages, or the pages that move
   int* to;      // [n_pages] compact: where they go
@@ -291,7 +291,13 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_fork(const __grid_consta
     return s >= 0 && s < a.n_rows && d >= 0 && d < a.n_rows && tokens_ok(a, a.tokens[s]) &&
            a.tokens[d] == 0 && s != d;
   };
-  // a row named twice goes to the first pair that names it
+  // a row named twice goes to the first pair that names it.  (The claims may hold what a call
+  // for a cache of fewer rows left there.)
+  for (int i = t; i < a.n; i += kPlanThreads) {
+    const int d = a.dst[i];
+    if (d >= 0 && d < a.n_rows) a.claim[d] = 0;
+  }
+  __syncthreads();
   for (int i = t; i < a.n; i += kPlanThreads)
     if (usable(i)) atomicMax(a.claim + a.dst[i], a.n - i);
   __syncthreads();
