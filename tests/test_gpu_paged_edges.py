@@ -1,10 +1,12 @@
 """Serving from a paged cache where the calls meet one another or the ends of
 their types: one workspace for caches of several sizes."""
+import numpy as np
 import pytest
 import torch
 
 from oracle import paged as op
 from test_gpu_kv_pages import Cache, _ints
+from test_gpu_paged import Case, D, _ws
 from weight_streaming_gemv_bf16_gb300 import binding as wb
 
 pytestmark = pytest.mark.gpu
@@ -57,3 +59,37 @@ def test_one_workspace_for_caches_of_few_and_of_many_rows(last):
         _resize(many, [-1] * 3 + [0] * 297, ws)
         _compact(many, ws)
         _resize(few, [16 * 100, 33, 0, 0], ws)
+
+
+# --------------------------------------------------------------------------- attention
+
+def _one_hot_keys(c, dims, sizes):
+    """Slot j's key: sizes[j] in dimension dims[j] (one power of two times a short fraction), zeros
+    elsewhere; the last slot is the new row.  Products with it are exact, and so are their sums."""
+    c.kp[c.kp == c.kp] = 0.0
+    n = c.pos[0] + 1
+    for j in range(n):
+        if j < n - 1:
+            c.kp[c.table[0][j // c.ps], :, j % c.ps, dims[j]] = sizes[j]
+    c.kn[:] = 0.0
+    c.kn.view(-1, c.nkv, D)[:, :, dims[n - 1]] = sizes[n - 1]
+    return c
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("size", [2.0 ** 60, 2.0 ** 110, 2.0 ** 118, 2.0 ** 126, 1.5 * 2.0 ** 127])
+def test_fp32_queries_of_any_size(dtype, size):
+    """Finite scores, the largest 2^-6 of itself and more above the others: its slot's value to the
+    bit, and the log-sum-exp that score, off by the queries' 2^-22 and four roundings (2^-22)."""
+    n = 40
+    c = Case([n - 1], 2, 1, 16, dtype, seed=31)
+    c.q[:] = size
+    c.q[:, 1::2] *= -1.0
+    _one_hot_keys(c, [2 * j for j in range(n)], [2.0 ** -14 * (1 + j / 64) for j in range(n)])
+    c.device()
+    c.call(_ws(2, 1))
+    best = c.vn[0].to(c.dt).float()
+    ref = size * 2.0 ** -14 * (1 + (n - 1) / 64) / D ** 0.5
+    for h in range(2):
+        assert torch.equal(c.o32[0, h * D:(h + 1) * D].cpu(), best)
+    assert (c.lse.cpu().double() / ref - 1).abs().max() <= 2.0 ** -21

@@ -240,8 +240,8 @@ struct PgCore {
     float up = 1.f;
     if constexpr (LO) {
       if constexpr (DT == DT_F16) {
-        // fp32 queries may lie outside fp16: each head by the power of two that
-        // brings its largest value to 1 .. 2
+        // fp32 queries may lie outside fp16: each head by the power of two that brings its
+        // largest value to 1 .. 2 (2 .. 4 from 2^127 on; 2^126 is the largest whose reciprocal is normal)
         float top = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -249,7 +249,7 @@ struct PgCore {
           for (int e = 0; e < 2; ++e) top = fmaxf(top, fmaxf(fabsf(x[i][e].x), fabsf(x[i][e].y)));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 100);
+        const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 126);
         up = __uint_as_float((uint32_t)(ex + 127) << 23);
         const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
 #pragma unroll
