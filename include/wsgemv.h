@@ -355,9 +355,11 @@ ws_status ws_token_logprobs(const void *logits, int dtype, long long ld, const i
  * they are; a position past the table's row, or a row outside the table, skips
  * the batch row and raises the device error flag (2); a page outside 0 ..
  * n_pages - 1 at or before pos[b] raises it too and makes the row's outputs NaN.  Slots after pos[b] are
- * never used (they may hold anything); a key or value that is not finite makes
- * the outputs of its own rows so (an infinite one as NaN).  Two batch rows must not write to one
- * slot, nor one to a slot that another reads.  fp32 queries
+ * never used (they may hold anything).  A value that is not finite makes that dimension
+ * of its own row's outputs so (an infinite one infinite or NaN).  A key that is not counts as its
+ * scores do: one of NaN or +infinity makes that head's outputs NaN, one of -infinity has weight
+ * 0 (with fp32 queries it may come out NaN: their terms differ in sign, or one is 0).  Two batch
+ * rows must not write to one slot, nor one to a slot that another reads.  fp32 queries
  * enter the products as two (fp16) or three (bf16) terms of the pages' type (relative
  * error 2^-22 of a head's largest value, 2^-24), the probabilities as hi + lo pairs
  * (2^-22, 2^-17), the rest is fp32.  out_f32 and/or out_16 (the pages' type) [B][n_heads * 128];

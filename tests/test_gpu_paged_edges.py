@@ -93,3 +93,31 @@ def test_fp32_queries_of_any_size(dtype, size):
     for h in range(2):
         assert torch.equal(c.o32[0, h * D:(h + 1) * D].cpu(), best)
     assert (c.lse.cpu().double() / ref - 1).abs().max() <= 2.0 ** -21
+
+
+@pytest.mark.parametrize("dtype,q", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "f32"), ("f16", "f32")])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_an_infinite_key_counts_as_its_scores_do(sign, dtype, q):
+    """Head 0's score of slot 19 is -infinity: weight 0, what the other slots give (or NaN, where an
+    fp32 query's terms differ in sign or one of them is 0); head 1's is +infinity: NaN.  The
+    tolerance is that of finite keys."""
+    c = Case([40], 2, 1, 16, dtype, q, seed=32)
+    c.kp[c.table[0][1], 0, 3, 5] = sign * float("inf")
+    c.q[0, 5], c.q[0, D + 5] = -sign, sign
+    c.device()
+    c.call(_ws(2, 1))
+    pages = torch.tensor(c.table[0])
+    K, V = (x[pages, 0].reshape(-1, D)[:41].double().numpy() for x in (c.kp, c.vp))
+    K[40], V[40] = (x[0].to(c.dt).double().numpy() for x in (c.kn, c.vn))
+    rest = np.arange(41) != 19
+    s = K[rest] @ c.q[0, :D].double().numpy() / np.sqrt(D)
+    top = (np.abs(K[rest]) @ np.abs(c.q[0, :D].double().numpy())).max() / np.sqrt(D)
+    e = np.exp(s - s.max())
+    out, mag = e / e.sum() @ V[rest], e / e.sum() @ np.abs(V[rest])
+    got, lse = c.o32.cpu().double().numpy()[0], c.lse.cpu().double().numpy()[0]
+    assert np.isnan(got[D:]).all() and np.isnan(lse[1])
+    if q == "f32" and np.isnan(lse[0]):
+        assert np.isnan(got[:D]).all()
+        return
+    assert (np.abs(got[:D] - out) <= mag * 2.0 ** -15 * (top + 1)).all()
+    assert abs(lse[0] - s.max() - np.log(e.sum())) <= 2.0 ** -16 * top + 2.0 ** -18 + 2.0 ** -21 * abs(lse[0])
