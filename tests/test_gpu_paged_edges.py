@@ -121,3 +121,35 @@ def test_an_infinite_key_counts_as_its_scores_do(sign, dtype, q):
         return
     assert (np.abs(got[:D] - out) <= mag * 2.0 ** -15 * (top + 1)).all()
     assert abs(lse[0] - s.max() - np.log(e.sum())) <= 2.0 ** -16 * top + 2.0 ** -18 + 2.0 ** -21 * abs(lse[0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("n", [1, 2, 40])
+def test_fp32_queries_enter_with_all_their_terms(n, dtype):
+    """Keys with one element each, so that no sum is rounded: what is left is the queries' terms.  A
+    query of 1 + 2^-9 + 2^-17 - 2^-23 takes three bf16 terms (exactly) or two fp16 ones (to 2^-22).
+    Scores then carry the scale's rounding, the product's, its difference from the maximum's and
+    the change of base: 4 x 2^-24 of the largest (2^-22), in fp16 twice that; the log-sum-exp two
+    more of its own, and exp2, the sum and the logarithm a few 2^-22 (2^-19).  So 2^-20 top +
+    2^-19; with one term fewer the scores are off by 2^-17 of themselves, which is 4 times as much
+    as that and more (checked here in 64 bits)."""
+    c = Case([n - 1], 2, 1, 16, dtype, seed=33)
+    r = np.random.default_rng(n)
+    x = 1 + 2.0 ** -9 + 2.0 ** -17 - 2.0 ** -23
+    c.q[:] = torch.from_numpy(x * r.choice([-1.0, 1.0], c.q.shape)).float()
+    sizes = r.choice([256.0, 512.0, 1024.0, 2048.0], n)
+    sizes[r.integers(n)] = 4096.0
+    _one_hot_keys(c, r.permutation(D)[:n].tolist(), sizes.tolist())
+    c.device()
+    c.call(_ws(2, 1))
+    (out, mag, lse, top), _, _ = c.oracle()
+    got, glse = c.o32.cpu().double().numpy().reshape(out.shape), c.lse.cpu().double().numpy()
+    tol = 2.0 ** -20 * top + 2.0 ** -19
+    assert (np.abs(glse - lse) <= tol).all()
+    # a probability moves by twice a score's error; the pairs' 2^-17, exp2 and the sums: 2^-16
+    assert (np.abs(got - out) <= mag * (2 * tol + 2.0 ** -16)[..., None]).all()
+    if dtype == "bf16":
+        hi = c.q.bfloat16().float()
+        c.q = hi + (c.q - hi).bfloat16().float()
+        (_, _, two, _), _, _ = c.oracle()
+        assert (np.abs(two - lse) >= 4 * tol)[np.abs(lse) > 0.7 * top].all()
