@@ -866,11 +866,13 @@ ws_status ws_empty_probe(int touch, const uint32_t *ptr, uint32_t *sink, ws_stre
  * arrives on, for timeout_ns, then records the time-out in the device error
  * flag and returns. */
 ws_status ws_test_bounded_wait(unsigned long long timeout_ns, ws_stream_t stream);
-/* Test hook for the waits inside ws_prompt_attention and ws_token_logprobs: in
- * launches from here on the CTA with index `cta` leaves out one copy, so that
- * the wait for it runs out (prompt attention: copies 0 and 1 are the queries of
- * its two tiles, 2 + 2 j and 3 + 2 j the keys and values of its block j;
- * log-probabilities: copy j is its step j); cta -1, the default: none. */
+/* Test hook for the waits inside ws_prompt_attention, ws_token_logprobs and
+ * ws_decode_attention_paged: in launches from here on the CTA with index `cta`
+ * leaves out one copy, so that the wait for it runs out (prompt attention:
+ * copies 0 and 1 are the queries of its two tiles, 2 + 2 j and 3 + 2 j the keys
+ * and values of its block j; log-probabilities: copy j is its step j; paged
+ * decode attention: copy j is slots 16 j .. 16 j + 15 of each row and head that
+ * it takes); cta -1, the default: none. */
 ws_status ws_test_withhold(int cta, int copy);
 
 const char *ws_version(void);

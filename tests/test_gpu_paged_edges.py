@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+from _util import tuning
 from oracle import paged as op
 from test_gpu_kv_pages import Cache, _ints
 from test_gpu_paged import Case, D, _ws
@@ -153,3 +154,41 @@ def test_fp32_queries_enter_with_all_their_terms(n, dtype):
         c.q = hi + (c.q - hi).bfloat16().float()
         (_, _, two, _), _, _ = c.oracle()
         assert (np.abs(two - lse) >= 4 * tol)[np.abs(lse) > 0.7 * top].all()
+
+
+# units of 16 slots that CTA 0 has: one of each warp; two a warp; three or four a warp, more than the
+# ring's stages; the only units of several rows, each of which it begins
+@pytest.mark.parametrize("q", ["f32", "bf16"])
+@pytest.mark.parametrize("pos,own,units", [([200, 100], [0], [0, 1, 3]), ([40000, 333], [0], [0, 5, 7]),
+                                           ([60000], [0], [0, 5, 8, 11]), ([15] * 1024, [0, 1, 2, 3], [0])])
+def test_a_copy_that_does_not_come(pos, own, units, q):
+    """The wait for it runs out: error 1, the rows of other CTAs as ever, and the call back within a
+    limit for each copy under way and one; the workspace serves the next call."""
+    limit_ms = 50
+    c = Case(pos, 2, 1, 64, "bf16", q, seed=34).device()
+    ws = _ws(2, 1, len(pos))
+    c.call(ws)
+    torch.cuda.synchronize()
+    whole = [x.clone() for x in (c.o32, c.o16, c.lse)]
+    rest = torch.tensor([b not in own for b in range(len(pos))])
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    for unit in units:
+        for x in (c.o32, c.o16, c.lse):
+            x.fill_(7.0)
+        with tuning(timeout_ns=limit_ms * 1_000_000):
+            wb.test_withhold(0, unit)
+            try:
+                begin.record()
+                c.call(ws)
+                end.record()
+                torch.cuda.synchronize()
+            finally:
+                wb.test_withhold(-1)
+        assert wb.device_error(reset=True) == 1, unit
+        assert limit_ms - 1 <= begin.elapsed_time(end) < 4.5 * limit_ms
+        for x, y in zip((c.o32, c.o16, c.lse), whole):
+            assert torch.equal(x[rest], y[rest]), unit
+        c.call(ws)
+        torch.cuda.synchronize()
+        for x, y in zip((c.o32, c.o16, c.lse), whole):
+            assert torch.equal(x, y), unit

@@ -90,6 +90,7 @@ struct PagedParams {
   unsigned* tick;      // [3][kPgMaxCtas]
   int* err;
   unsigned long long timeout_ns;
+  TestHold hold;       // copies: the units of a row and part
 };
 
 // A batch row's sequence: its table row and last slot; pos < 0: none.
@@ -531,6 +532,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtas<LO>)
       ent_next = pages_of(next);
     }
     const int page = __shfl_sync(all, ent, 0), in = (unit - pg_page(a, unit) * a.upp) * kPgUnit;
+    const bool held = unit == a.hold.here();
     ent = __shfl_down_sync(all, ent, 1);
     --left;
     unit += kPgWarps;
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtas<LO>)
     if ((unsigned)page >= (unsigned)a.n_pages) {
       bad |= 1u << ni;
       if (lane == 0) atomicExch(a.err, kDerrBadSlot);
-    } else if (lane == 0) {
+    } else if (lane == 0 && !held) {
       const int row = (page * a.nkv + pg_head(a, part)) * a.ps + in;
       mbar_arrive_expect_tx(bar, kPgStageBytes);
       tma_load_3d(st, &a.mk, 0, row, 0, bar);
@@ -842,6 +844,7 @@ ws_status ws_decode_attention_paged(const void *q, int q_dtype, const void *k_ne
   a.tick = static_cast<unsigned*>(workspace);
   a.part = reinterpret_cast<float*>(a.tick + 3 * kPgMaxCtas);
   a.timeout_ns = tuning().timeout_ns;
+  a.hold = test_hold();
   a.err = device_error_ptr();
   if (!a.err) {
     set_error("device error flag unavailable");
