@@ -1,5 +1,7 @@
 """Serving from a paged cache where the calls meet one another or the ends of
-their types: one workspace for caches of several sizes."""
+their types and sizes: one workspace for caches of several sizes, queries and keys
+at the ends of their types, copies that do not come, offsets beyond 32 bits.
+Tolerances are test_gpu_paged's where none is given."""
 import numpy as np
 import pytest
 import torch
@@ -7,7 +9,7 @@ import torch
 from _util import tuning
 from oracle import paged as op
 from test_gpu_kv_pages import Cache, _ints
-from test_gpu_paged import Case, D, _ws
+from test_gpu_paged import DT, Case, D, _ws
 from weight_streaming_gemv_bf16_gb300 import binding as wb
 
 pytestmark = pytest.mark.gpu
@@ -192,3 +194,90 @@ def test_a_copy_that_does_not_come(pos, own, units, q):
         torch.cuda.synchronize()
         for x, y in zip((c.o32, c.o16, c.lse), whole):
             assert torch.equal(x, y), unit
+
+
+def test_one_table_row_read_by_several_batch_rows():
+    """Without new rows a sequence may be read any number of times, to other lengths too."""
+    c = Case([40, 200], 4, 2, 32, seed=35, rows=[0, 1], new=False)
+    c.pos, c.rows = [200, 64, 200, 13], [1, 1, 1, 0]
+    c.q = torch.cat([c.q, -c.q])
+    c.device()
+    c.call(_ws(4, 2, 4))
+    c.check()
+
+
+def test_pages_beyond_32_bits():
+    """A cache of more than 2^31 elements, its last pages in use: stored into, read, brought down."""
+    nkv, ps = 2, 64
+    n_pages = (1 << 24) // (nkv * ps) + 700
+    c = Case([150, 63], 4, nkv, ps, seed=36)
+    low = {p for row in c.table for p in row if p >= 0}
+    up = {p: n_pages - 1 - 3 * i for i, p in enumerate(sorted(low))}
+    kp, vp = (wb.new_kv_pages(n_pages, nkv, ps) for _ in range(2))
+    table, refs, tokens = wb.new_page_table(2, len(c.table[0]), n_pages)
+    table.copy_(_ints([[up.get(p, -1) for p in row] for row in c.table]))
+    for p, at in up.items():
+        refs[at] = 1
+    # the rows' tokens but the last through the store, the last by the attention
+    for b, n in enumerate(c.pos):
+        pages = torch.tensor(c.table[b][:n // ps + 1])
+        k, v = (x[pages].transpose(1, 2).reshape(-1, nkv, D)[:n].contiguous().cuda() for x in (c.kp, c.vp))
+        wb.kv_store_paged(k, v, kp, vp, table, _ints([0]), cu_seqlens=_ints([0, n]), rows=_ints([b]))
+    c.device()
+    c.d[3:] = [kp, vp]
+    c.dtable = table
+
+    def check():
+        (out, mag, lse, top), hk, hv = c.oracle()
+        got = c.o32.cpu().double().numpy().reshape(out.shape)
+        assert (np.abs(got - out) <= mag * 2.0 ** -15 * (top[..., None] + 1)).all()
+        for b, n in enumerate(c.pos):
+            for j, page in enumerate(table[b].tolist()[:n // ps + 1]):
+                held = min(ps, n + 1 - j * ps)
+                for dev, host in ((kp, hk), (vp, hv)):
+                    assert np.array_equal(dev[page, :, :held].cpu().double().numpy(), host[c.table[b][j], :, :held])
+
+    c.call(_ws(4, nkv))
+    check()
+    ws = torch.zeros(wb.kv_pages_workspace_bytes(2, n_pages), dtype=torch.uint8, device="cuda")
+    wb.kv_pages_compact(table, refs, kp, vp, ws)
+    n = len(up)
+    assert refs[:n].tolist() == [1] * n and int(refs.sum()) == n
+    assert sorted(p for p in table.flatten().tolist() if p >= 0) == list(range(n))
+    c.o32.fill_(7.0)
+    c.call(_ws(4, nkv))
+    check()
+
+
+# --------------------------------------------------------------------------- the store
+
+@pytest.mark.parametrize("src,dst", [("f32", "bf16"), ("bf16", "bf16"), ("f16", "f16")])
+@pytest.mark.parametrize("nkv", [1, 2, 3, 4, 5, 7])
+def test_store_of_several_tokens_a_warp(nkv, src, dst):
+    """More than 16384 (token, head) pairs of fewer than 8 heads; sequences that end inside a warp's
+    tokens, without a slot, and tokens behind the last; rows padded."""
+    g = torch.Generator().manual_seed(nkv)
+    lens = [1, 0, 7, 16400 // nkv, 3, 500, 64]
+    start = [5, 3, 0, 2, -1, 40, 0]
+    rows = [6, 5, 4, 3, 2, 1, 0]
+    cu = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    T, ps = cu[-1] + 5, 48
+    max_pages = max(lens) // ps + 2
+    n_pages = 7 * max_pages
+    table = torch.randperm(n_pages, generator=g).view(7, max_pages).int()
+    wide = torch.randn(T, nkv + 1, D, generator=g).to(DT[src]).cuda()
+    k = wide[:, :nkv]
+    v = (wide * 2)[:, 1:]
+    kp = torch.full((n_pages, nkv, ps, D), 7.0, dtype=DT[dst], device="cuda")
+    vp = kp.clone()
+    rk, rv = kp.clone(), vp.clone()
+    wb.kv_store_paged(k, v, kp, vp, table.cuda(), _ints(start), cu_seqlens=_ints(cu), rows=_ints(rows))
+    for i, n in enumerate(lens):
+        if start[i] < 0 or n == 0:
+            continue
+        slot = torch.arange(start[i], start[i] + n)
+        page = table[rows[i]].long()[slot // ps].cuda()
+        at = (slot % ps).cuda()
+        rk[page, :, at] = k[cu[i]:cu[i + 1]].to(DT[dst])
+        rv[page, :, at] = v[cu[i]:cu[i + 1]].to(DT[dst])
+    assert torch.equal(kp, rk) and torch.equal(vp, rv)

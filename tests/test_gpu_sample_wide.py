@@ -1,6 +1,6 @@
 """The drawing of tokens where few rows of a large vocabulary lie on the device: up
 to 4 rows of 131072 tokens and more are cut over 16 CTAs each, more rows over 8.
-Tolerances are test_gpu_sample's."""
+And logits whose offsets pass 32 bits.  Tolerances are test_gpu_sample's."""
 import numpy as np
 import pytest
 import torch
@@ -75,3 +75,25 @@ def test_one_logit_that_rules_a_row_out(at):
         for s in SETTINGS:
             token, prob = _draw(x, u, **s)
             assert token[1] == -1 and np.isnan(prob[1]) and (token[[0, 2]] >= 0).all()
+
+
+def test_logits_beyond_32_bits():
+    """More than 2^31 logits: the last rows are drawn as they are alone."""
+    V, rows = 151936, 14200
+    some, u = _logits(8, V, "bf16", seed=6)
+    x = some.repeat(rows // 8, 1)
+    assert x.numel() > 1 << 31
+    s = dict(temperature=0.9, top_p=0.95)
+    token, prob = _draw(x, u * (rows // 8), **s)
+    t, p = _draw(some, u, **s)
+    assert np.array_equal(token, np.tile(t, rows // 8)) and np.array_equal(prob, np.tile(p, rows // 8))
+
+
+@pytest.mark.parametrize("V", [700, 5000, 151936])
+def test_zeros_of_both_signs_in_the_settings(V):
+    x, u = _logits(2, V, "f32", seed=7)
+    for s in (dict(top_p=0.0), dict(min_p=0.0), dict(temperature=0.0), dict(top_p=0.0, top_k=40)):
+        token, prob = _draw(x, [0.0, 0.0], **s)
+        other, q = _draw(x, [-0.0, -0.0], **{n: v if n == "top_k" else -0.0 for n, v in s.items()})
+        assert np.array_equal(token, other) and np.array_equal(prob, q)
+        assert (token >= 0).all()
