@@ -422,9 +422,9 @@ ws_status ws_kv_store_paged(const void *k, const void *v, int src_dtype, const i
  * pages from L on are free afterwards.
  *
  * The pages' data: k_pages and v_pages [layers][n_pages] pages of page_bytes
- * bytes (a multiple of 16, to 2^30), one table for all layers; any type that is laid out
- * page by page (bf16, fp16, the 4-bit rows of ws_kv_store_q4).  refs, pages and
- * workspace 16-byte aligned.  Workspace (zero-filled before its first use, left ready
+ * bytes (a multiple of 16, to 2^30), one table for all layers; they are moved as bytes,
+ * whatever their type (ws_kv_store_paged and ws_decode_attention_paged have bf16 and fp16).
+ * refs, pages and workspace 16-byte aligned.  Workspace (zero-filled before its first use, left ready
  * by every call): ws_kv_pages_workspace_bytes(n_rows, n_pages); one that is large enough
  * serves caches of several sizes in turn; calls that share one, or a table, must
  * not overlap. */

@@ -12,7 +12,7 @@
 // Bound by latency: the plan reads every count (four bytes a page) through one
 // SM, 16 a thread at a time, until it has enough; then by DRAM: the moved pages.  64 rows
 // resized, 16384 pages: 9.5 us; 256 rows, 300000 pages: 24.5; 16 rows, 1024 pages: 6.3.  64
-// children forked, 28 layers: 31 us.  A cache of 2048 pages, 8 layers compacted: the plan 8 us,
+// children forked, 28 layers: 31.5 us.  A cache of 2048 pages, 8 layers compacted: the plan 8 us,
 // 528 MB read and as much written in 157, 6.7 TB/s, 0.99 of the copy rate.
 #include "ws_kv_q4.cuh"
 #include "ws_paged.cuh"
