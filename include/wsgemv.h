@@ -32,9 +32,12 @@
  *    memory (then a NULL workspace gives WS_ERR_ARG).  Size it with
  *    ws_workspace_bytes().
  *  - A workspace must be zero-filled before its first use; the library
- *    leaves it zeroed again after every successful call, so one workspace
- *    serves any number of calls ordered on one stream.  Calls that share a
- *    workspace must not overlap in time.
+ *    leaves it ready for the next call, so one workspace serves any number of
+ *    calls ordered on one stream, of several operators and sizes that it is
+ *    large enough for (16 KB of it hold counters, zero between calls).
+ *    ws_decode_attention and the serving operators leave theirs ready for
+ *    their own next call only, as they say.  Calls that share a workspace must
+ *    not overlap in time.
  *  - Device-side waits are bounded; a wait that runs out sets a device error
  *    flag read by ws_device_error() and the kernel returns.
  *  - No exception crosses the ABI.  ws_last_error() gives a thread-local
@@ -204,7 +207,9 @@ ws_status ws_lmhead_argmax(const void *h, int h_dtype, const void *gamma, const 
  * (row, key-value head) is cut into splits of whole 64-slot runs, as many as
  * fill one wave of CTAs; the last split of each group of 16 merges the
  * group's partial softmax results and the last group merges the groups.
- * Workspace (zero-filled before its first use, left zeroed by every call):
+ * Workspace (zero-filled before its first use, left ready for the next call of
+ * this operator with the same B, heads and s_max; zero-filled again before one
+ * with others, whose counters may lie where partial results are):
  * ws_attention_workspace_bytes(B, n_heads, n_kv_heads, 128, s_max). */
 size_t ws_attention_workspace_bytes(int B, int n_heads, int n_kv_heads, int head_dim, int s_max);
 ws_status ws_decode_attention(const float *q, const float *k_new, const float *v_new,

@@ -313,6 +313,13 @@ int device_sm_count();
 int* device_error_ptr();
 void set_error(const char* fmt, ...);
 bool plan_gemv(GemvParams& p, int force_S, char* why, size_t why_len);
+// A workspace's first bytes hold tickets alone, whatever the operator and its sizes: what a call
+// leaves behind them (partial sums and maxima) never lies where another one's tickets are.  A
+// call with more of them has the rest cleared before its launch (clear_tickets), the rare large
+// one: 4096 row groups split along K, or rows.  In place of the partial sums left zeroed, which
+// cost calls of 6 to 8 us 0.3 to 0.7.
+constexpr size_t kTicketBytes = 16384;
+cudaError_t clear_tickets(void* ws, size_t tickets, cudaStream_t stream);
 size_t workspace_layout(const GemvParams& p, size_t* off_tickets, size_t* off_part,
                         size_t* off_argv, size_t* off_argi, size_t* off_argt);
 bool bind_workspace(GemvParams& p, void* ws, size_t ws_bytes);

@@ -580,13 +580,23 @@ bool plan_gemv(GemvParams& p, int force_S, char* why, size_t why_len) {
 
 static size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
+static size_t ticket_count(const GemvParams& p) {
+  return (p.sc.S > 1 ? (size_t)p.sc.RG : 0) + (p.epilogue == EPI_ARGMAX ? 1 : 0);
+}
+
+cudaError_t clear_tickets(void* ws, size_t tickets, cudaStream_t stream) {
+  if (tickets * 4 <= kTicketBytes) return cudaSuccess;
+  return cudaMemsetAsync(static_cast<char*>(ws) + kTicketBytes, 0, align256(tickets * 4) - kTicketBytes, stream);
+}
+
 size_t workspace_layout(const GemvParams& p, size_t* off_tickets, size_t* off_part,
                         size_t* off_argv, size_t* off_argi, size_t* off_argt) {
-  size_t off = 0;
+  // the row groups' tickets, then the argmax's, the last of the tickets' bytes
+  const size_t n = ticket_count(p);
+  size_t off = n * 4 > kTicketBytes ? align256(n * 4) : n ? kTicketBytes : 0;
   size_t t = 0, pt = 0, av = 0, ai = 0, at = 0;
+  if (p.epilogue == EPI_ARGMAX) at = off - 4;
   if (p.sc.S > 1) {
-    t = off;
-    off = align256(off + (size_t)p.sc.RG * 4);
     pt = off;
     off = align256(off + (size_t)p.sc.S * p.nmat * p.B * p.M_total * 4);
   }
@@ -595,8 +605,6 @@ size_t workspace_layout(const GemvParams& p, size_t* off_tickets, size_t* off_pa
     off = align256(off + (size_t)p.sc.grid * p.B * 4);
     ai = off;
     off = align256(off + (size_t)p.sc.grid * p.B * 4);
-    at = off;
-    off = align256(off + 4);
   }
   if (off_tickets) *off_tickets = t;
   if (off_part) *off_part = pt;
@@ -770,7 +778,10 @@ static ws_status plan_bind_launch(GemvParams& p, void* ws, size_t ws_bytes, cuda
       return WS_ERR_ARG;
     }
   }
-  const cudaError_t e = launch_gemv(p, st, tuning().launch_pdl != 0);
+  // (a kernel behind a cleared workspace is no programmatic dependent of one)
+  const size_t tickets = ticket_count(p);
+  cudaError_t e = clear_tickets(ws, tickets, st);
+  if (e == cudaSuccess) e = launch_gemv(p, st, tuning().launch_pdl != 0 && tickets * 4 <= kTicketBytes);
   if (e != cudaSuccess) {
     set_error("launch failed: %s", cudaGetErrorString(e));
     return WS_ERR_CUDA;

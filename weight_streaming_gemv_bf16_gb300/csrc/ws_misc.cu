@@ -284,12 +284,16 @@ TestHold& test_hold() {
   return hold;
 }
 
+static size_t argmax_rows_tickets(int rows) {
+  const size_t t = ((size_t)rows * 4 + 255) / 256 * 256;
+  return t > kTicketBytes ? t : kTicketBytes;
+}
+
 size_t argmax_rows_workspace(int rows, int cols) {
   if (rows <= 0 || cols <= 0) return 0;
   const size_t cb = (size_t)argmax_cols_per_row_blocks(cols);
   const size_t a = ((size_t)rows * cb * 4 + 255) / 256 * 256;
-  const size_t t = ((size_t)rows * 4 + 255) / 256 * 256;
-  return 2 * a + t;
+  return 2 * a + argmax_rows_tickets(rows);
 }
 
 }  // namespace ws
@@ -360,10 +364,15 @@ ws_status ws_argmax_rows(const float* logits, int32_t* idx, int rows, int cols, 
   }
   const int cb = argmax_cols_per_row_blocks(cols);
   const size_t a = ((size_t)rows * cb * 4 + 255) / 256 * 256;
-  char* base = static_cast<char*>(workspace);
+  unsigned* tickets = static_cast<unsigned*>(workspace);
+  char* base = static_cast<char*>(workspace) + argmax_rows_tickets(rows);
   float* pv = reinterpret_cast<float*>(base);
   int* pi = reinterpret_cast<int*>(base + a);
-  unsigned* tickets = reinterpret_cast<unsigned*>(base + 2 * a);
+  const cudaError_t e = clear_tickets(workspace, rows, (cudaStream_t)stream);
+  if (e != cudaSuccess) {
+    set_error("clearing the tickets failed: %s", cudaGetErrorString(e));
+    return WS_ERR_CUDA;
+  }
   k_argmax_rows<<<dim3(cb, rows), 256, 0, (cudaStream_t)stream>>>(logits, idx, rows, cols, pv,
                                                                    pi, tickets);
   return launch_status();

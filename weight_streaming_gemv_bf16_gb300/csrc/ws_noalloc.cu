@@ -30,7 +30,8 @@
 
 namespace ws {
 
-constexpr size_t kNoAllocScratchBytes = 1u << 20;  // 1 MiB
+constexpr size_t kNoAllocMost = 1u << 20;  // 1 MiB of partial sums and the tickets that a shape takes
+constexpr size_t kNoAllocScratchBytes = kNoAllocMost + kTicketBytes;
 
 static __device__ __align__(256) unsigned char g_noalloc_scratch[kNoAllocScratchBytes];
 
@@ -96,10 +97,11 @@ extern "C" ws_status ws_gemv_bf16_noalloc(const void* W, const void* x, float* y
   }
   size_t off_tickets = 0, off_part = 0;
   const size_t need = workspace_layout(p, &off_tickets, &off_part, nullptr, nullptr, nullptr);
-  if (need > kNoAllocScratchBytes) {
+  const size_t most = need > 0 ? need - off_part + ((size_t)p.sc.RG * 4 + 255) / 256 * 256 : 0;
+  if (most > kNoAllocMost) {
     set_error("M=%d K=%d B=%d needs %zu bytes of split-K scratch; the fixed scratch array "
               "holds %zu bytes (use ws_gemv_bf16 with a workspace)",
-              M, K, B, need, kNoAllocScratchBytes);
+              M, K, B, most, kNoAllocMost);
     return WS_ERR_SHAPE;
   }
   cudaStream_t st = (cudaStream_t)stream;
