@@ -1593,8 +1593,12 @@ static int sp_stay(int per, int vec) { return (per + 2 * vec - 2) / vec * 16; }
 // 151936 fp32 in four 62, 73, in two 89, 101; but 76 rows of bf16 in four, which do not fit, 87, 66,
 // in two 57, 73.  Slices of 32768 also where pairs of CTAs take two waves, the costly rows first: whole
 // rows are all resident, and an SM with two costly ones holds up the rest.  256 rows of 151936
-// bf16 in two 163, 98, whole 142, 150 (without settings 107 and 91: whole).  But 256 of 32000 in two 79, 56,
-// whole 52, 67; 500 of 50257 fp32 174, 126 and 144, 104.
+// bf16 in two 163, 98, whole 142, 150 (without settings 107 and 91: whole).  160 to 300 rows of
+// 65536, 100000 and 151936: settings of every kind bf16 60 to 115 in two and 83 to 158 whole, fp32
+// 79 to 163 and 112 to 309; top_p 0.9 for all bf16 81 to 168 and 72 to 144, fp32 87 to 187 and 79 to
+// 172; the largest of all 18 to 64 and 13 to 67: what one setting for all loses (a quarter to a half
+// at 65536, little at 151936) is less than what different ones gain, and which it is only the device
+// knows.  But 256 of 32000 in two 79, 56, whole 52, 67; 500 of 50257 fp32 174, 126 and 144, 104.
 template <int DT>
 static cudaError_t sample_launch(SampleParams p, cudaStream_t stream) {
   if (p.V <= kSpWhole) return launch_serving(k_sample_whole<DT>, dim3((unsigned)p.rows), kSpWholeThreads, 0, stream, p);
