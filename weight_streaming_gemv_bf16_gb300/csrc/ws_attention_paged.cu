@@ -10,7 +10,7 @@
 // cache's type that they take (three in bf16, two in fp16: relative error 2^-24 and
 // 2^-22), so that the log-sum-exp is as good as fp32; the probabilities as hi + lo pairs
 // (2^-17, 2^-22), as in the decode attention over contiguous caches: bf16 outputs before their
-// rounding (2^-9) are off by 2e-6 of themselves (root mean square, 64 rows to 2111).  A third bf16
+// rounding (2^-9) are off by 2e-6 of themselves (root mean square, rows of 2111).  A third bf16
 // term was built: 3e-7, half as many value products again, 0.4 to 1.1% of the time of the batches
 // below.
 //
